@@ -411,3 +411,7 @@ def layers_run(layers, xs, ys, workspace=None, stream=None):
     ws, wsb = _workspace(workspace, int(lib().skinny_layers_workspace_bytes(table, n, M)), "skinny_layers_run")
     _check(lib().skinny_layers_run(table, n, xp, yp, M, ws, wsb, _stream(stream)), "skinny_layers_run")
     return ys
+
+
+from .kv4 import (kv4_append, kv4_read, kv4_attention, kv4_attention_workspace_bytes, kv4_attention_weights,  # noqa: E402
+                  kv4_evict, lm_head_logprobs, lm_head_logprobs_workspace_bytes)

@@ -51,6 +51,14 @@ def _declare(lib):
         "skinny_layers_workspace_bytes": (c_size_t, [ctypes.POINTER(SkinnyLayer), c_int, c_int]),
         "skinny_layers_run": (c_int, [ctypes.POINTER(SkinnyLayer), c_int, ctypes.POINTER(P), ctypes.POINTER(P),
                                       c_int, P, c_size_t, P]),
+        "kv4_append": (c_int, [P, P, P, c_int, c_int, P]),
+        "kv4_read": (c_int, [P, P, P, c_int, c_int, P]),
+        "kv4_attention": (c_int, [P, P, c_int, c_int, c_int, c_float, P, P, P, c_size_t, P]),
+        "kv4_attention_workspace_bytes": (c_size_t, [c_int] * 6),
+        "kv4_attention_weights": (c_int, [P, P, c_int, c_int, c_int, c_float, P, P, P, P]),
+        "kv4_evict": (c_int, [P, P, P, P, P, P, c_int, c_int, c_int, P]),
+        "lm_head_logprobs": (c_int, [P, c_int, ctypes.c_int64, P, P, P, P, P, c_int, c_int, c_int, P, c_size_t, P]),
+        "lm_head_logprobs_workspace_bytes": (c_size_t, [c_int] * 3),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -86,4 +94,6 @@ EXPORTED = ("nvfp4_pack", "nvfp4_gemm", "fp8_gemm", "lm_head_gemm_argmax", "nvfp
             "nvfp4_gemm_swiglu_config", "lm_head_verify_greedy", "lm_head_verify_greedy_config",
             "skinny_layers_workspace_bytes", "skinny_layers_run", "fp8_pack", "fp8_gemm_packed",
             "fp8_gemm_packed_config", "skinny_default_config", "nvfp4_gemm_noalloc",
-            "skinny_read_probe_pattern")
+            "skinny_read_probe_pattern", "kv4_append", "kv4_read", "kv4_attention",
+            "kv4_attention_workspace_bytes", "kv4_attention_weights", "kv4_evict", "lm_head_logprobs",
+            "lm_head_logprobs_workspace_bytes")

@@ -21,7 +21,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libskinny.so")
-SOURCES = ["host.cpp", "nvfp4_gemm.hip", "fp8_gemm.hip", "reduce.hip", "probe.hip", "noalloc.hip"]
+SOURCES = ["host.cpp", "nvfp4_gemm.hip", "fp8_gemm.hip", "reduce.hip", "probe.hip", "noalloc.hip",
+           "kv4_host.cpp", "kv4_cache.hip", "kv4_attention.hip", "logprobs.hip"]
 ARCH = "gfx950"
 
 # Kernels known to spill, with their scratch bytes per lane: the streaming

@@ -1,0 +1,123 @@
+// Device helpers of the 4-bit key/value cache: the places of a token's bytes
+// in a page's block (the layout is in skinny.h), element types, page lookup.
+#ifndef SKINNY_KV4_CUH
+#define SKINNY_KV4_CUH
+
+#include <hip/hip_bf16.h>
+
+#include "common.cuh"
+#include "skinny.h"
+
+namespace skinny {
+
+constexpr int kPage = SKINNY_KV_PAGE;
+
+// Offsets of a block's four parts for head size D.
+template <int D>
+struct KvBlock {
+  static constexpr int kKScales = 32 * D;
+  static constexpr int kVCodes = 36 * D;
+  static constexpr int kVScales = 68 * D;
+  static constexpr int kBytes = 72 * D;
+  static constexpr int kGroups = D / 16;  // scales per token, also positions per V column block
+
+  // Scale byte of token t's group f (16 positions).
+  __host__ __device__ static int k_scale(int t, int f) {
+    return kKScales + ((f / (D / 64)) * 16 + t % 16) * (D / 16) + (t / 16) * (D / 64) + f % (D / 64);
+  }
+  __host__ __device__ static int v_scale(int t, int f) {
+    return kVScales + f * 64 + (t % 16 / 4) * 16 + (t / 16) * 4 + t % 4;
+  }
+  // The eight code bytes of token t's group f of K lie together.
+  __host__ __device__ static int k_codes(int t, int f) {
+    const int run = (t / 16) * (D / 8) + (f % (D / 64)) * 8;
+    return (run / 16) * 1024 + (f / (D / 64)) * 256 + (t % 16) * 16 + run % 16;
+  }
+  // Of V, 256 / D column blocks of D / 32 bytes each, 16 bytes apart; this is the first.
+  __host__ __device__ static int v_codes(int t, int f) {
+    const int run = ((t / 16) * 4 + t % 4) * (D / 32);
+    return kVCodes + (run / 16) * 1024 + (t % 16 / 4) * 256 + f * (256 / D) * 16 + run % 16;
+  }
+};
+
+// The eight code bytes of token t's group f, from or to a block in global
+// memory or LDS.
+template <int D>
+__device__ __forceinline__ u32x2 kv_codes_load(const uint8_t* block, int t, int f, bool v) {
+  if (!v) return *reinterpret_cast<const u32x2*>(block + KvBlock<D>::k_codes(t, f));
+  const uint8_t* p = block + KvBlock<D>::v_codes(t, f);
+  if constexpr (D == 256) {
+    return *reinterpret_cast<const u32x2*>(p);
+  } else if constexpr (D == 128) {
+    return u32x2{*reinterpret_cast<const uint32_t*>(p), *reinterpret_cast<const uint32_t*>(p + 16)};
+  } else {
+    const auto h = [&](int i) { return static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p + 16 * i)); };
+    return u32x2{h(0) | (h(1) << 16), h(2) | (h(3) << 16)};
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void kv_codes_store(uint8_t* block, int t, int f, bool v, u32x2 c) {
+  if (!v) {
+    *reinterpret_cast<u32x2*>(block + KvBlock<D>::k_codes(t, f)) = c;
+    return;
+  }
+  uint8_t* p = block + KvBlock<D>::v_codes(t, f);
+  if constexpr (D == 256) {
+    *reinterpret_cast<u32x2*>(p) = c;
+  } else if constexpr (D == 128) {
+    *reinterpret_cast<uint32_t*>(p) = c.x;
+    *reinterpret_cast<uint32_t*>(p + 16) = c.y;
+  } else {
+    *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(c.x);
+    *reinterpret_cast<uint16_t*>(p + 16) = static_cast<uint16_t>(c.x >> 16);
+    *reinterpret_cast<uint16_t*>(p + 32) = static_cast<uint16_t>(c.y);
+    *reinterpret_cast<uint16_t*>(p + 48) = static_cast<uint16_t>(c.y >> 16);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ int kv_scale_at(int t, int f, bool v) {
+  return v ? KvBlock<D>::v_scale(t, f) : KvBlock<D>::k_scale(t, f);
+}
+
+// The slots of sequence b, within what its table holds.
+__device__ __forceinline__ int kv_len(const kv4_cache& c, int b) {
+  const int n = c.lens[b];
+  return n < 0 ? 0 : (n > c.width * kPage ? c.width * kPage : n);
+}
+
+// The block of (page id, head), or null where the id names no page.
+template <int D>
+__device__ __forceinline__ uint8_t* kv_block(const kv4_cache& c, int id, int head) {
+  if (static_cast<unsigned>(id) >= static_cast<unsigned>(c.pages)) return nullptr;
+  return static_cast<uint8_t*>(c.data) + (static_cast<size_t>(id) * c.Hk + head) * KvBlock<D>::kBytes;
+}
+
+// 16-bit element types.
+struct F16 {
+  static __device__ __forceinline__ float load(uint32_t bits) {
+    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(bits)));
+  }
+  static __device__ __forceinline__ uint32_t store(float v) {
+    return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+  }
+};
+struct BF16 {
+  static __device__ __forceinline__ float load(uint32_t bits) { return __uint_as_float(bits << 16); }
+  static __device__ __forceinline__ uint32_t store(float v) {  // to the nearest, ties to even
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+  }
+};
+
+// Two elements of a dword, and back.
+template <class E>
+__device__ __forceinline__ float elem_lo(uint32_t w) { return E::load(w & 0xFFFFu); }
+template <class E>
+__device__ __forceinline__ float elem_hi(uint32_t w) { return E::load(w >> 16); }
+template <class E>
+__device__ __forceinline__ uint32_t elem_pack(float lo, float hi) { return E::store(lo) | (E::store(hi) << 16); }
+
+}  // namespace skinny
+
+#endif

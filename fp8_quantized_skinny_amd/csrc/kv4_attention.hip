@@ -1,0 +1,616 @@
+// Attention over the 4-bit key/value cache, and the attention weights it adds
+// to the slots.
+//
+// With S = scale q . K~ over the slots that a row sees:
+//   out = sum_j exp(S_j - m) v~_j / sum_j exp(S_j - m),  lse = m + log(sum)
+//   weight_j = sum over rows of exp(S_j - lse)
+//
+// A wavefront takes a page (64 tokens) of one key/value head for up to MT * 16
+// of the head's T * G query rows, so that codes are widened once for all of
+// them.  Both products run on v_mfma_f32_16x16x32_f16 in the transposed form:
+//   S^T[token][query] = K[token][d] Q^T[d][query]
+//   O^T[d][query]     = V^T[d][token] P^T[token][query]
+// The first leaves lane 16 g + c with query c's scores of tokens 4 g .. 4 g + 3
+// of a 16-token tile, which is how the second wants its right operand (any
+// order of the summed tokens serves as long as both operands have it), so P
+// never leaves its lanes, and the running maximum and sum of a query are values
+// of its own lanes.  The cache's byte order gives lane 16 g + c of every load
+// the K codes of token c's quarter g, and the V codes of tokens 4 g .. 4 g + 3
+// at positions c * D/16 ...
+#include <hip/hip_runtime.h>
+
+#include "internal.h"
+#include "kv4.cuh"
+
+namespace skinny {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kMinNormal = 0x1p-126f;
+// Weights go to fp16 times 2^kLift relative to the reference maximum, which
+// follows the running one only when that rose by more than 2^kSlack: weights
+// then stay below 2^(kLift + kSlack) = 2^14 and keep fp16's full precision
+// down to 2^-20 of the greatest, and a row's sums are rescaled rarely.
+constexpr float kLift = 6.0f, kSlack = 8.0f;
+
+struct AttendArgs {
+  kv4_cache c;
+  kv4_rows q;
+  void* out;
+  float* lse;
+  float* part;  // [segment * splits + split][MT * 16][D] sums, then the statistics
+  float* stat;  // [segment * splits + split][MT * 16][2]: reference maximum (log2), sum
+  int T, Hq, G, QG, splits;
+  float scale;
+};
+
+// As sum_over_rows, for the greatest.
+__device__ __forceinline__ float max_over_rows(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto h = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  v = fmaxf(__uint_as_float(h[0]), __uint_as_float(h[1]));
+  const uint32_t w = __float_as_uint(v);
+  const auto q = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+  return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+
+// LDS copy of a workgroup's query rows as fp16, row stride D + 8 halves (16
+// bytes off the banks' period).  bf16 rows are scaled by the power of two that
+// brings their greatest value to 2^14 .. 2^15; `factor` undoes it.
+template <int D, int MT, class E>
+__device__ __forceinline__ void stage_queries(const kv4_rows& q, int b, int h, int qg, int G, int R, _Float16* qs,
+                                              float* factor) {
+  constexpr int kPer = D / 8;  // threads per row
+  for (int i = threadIdx.x; i < MT * 16 * kPer; i += kThreads) {
+    const int row = i / kPer, piece = i % kPer;
+    const int r = qg * MT * 16 + row;
+    u32x4 w{0u, 0u, 0u, 0u};
+    if (r < R)
+      w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(q.data) + b * q.sequence + (r / G) * q.row +
+                                          (h * G + r % G) * q.head + piece * 8);
+    if constexpr (std::is_same_v<E, BF16>) {
+      float amax = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float lo = fabsf(elem_lo<E>(w[j])), hi = fabsf(elem_hi<E>(w[j]));
+        amax = lo < INFINITY ? fmaxf(amax, lo) : amax;
+        amax = hi < INFINITY ? fmaxf(amax, hi) : amax;
+      }
+#pragma unroll
+      for (int o = 1; o < kPer; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
+      int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+      ex = ex < -100 ? -100 : ex;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = elem_pack<F16>(ldexpf(elem_lo<E>(w[j]), 14 - ex), ldexpf(elem_hi<E>(w[j]), 14 - ex));
+      if (piece == 0) factor[row] = ldexpf(1.0f, ex - 14);
+    } else if (piece == 0) {
+      factor[row] = 1.0f;
+    }
+    *reinterpret_cast<u32x4*>(qs + row * (D + 8) + piece * 8) = w;
+  }
+}
+
+// A lane's part of a block: K and V codes and scales.
+template <int D>
+struct KRegs {
+  u32x4 codes[D / 32];
+  uint32_t scales[D / 64];
+  __device__ __forceinline__ void load(const uint8_t* block, int lane) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) codes[i] = load16(block + i * 1024 + lane * 16);
+    const uint8_t* s = block + KvBlock<D>::kKScales + lane * (D / 16);
+    if constexpr (D == 64) {
+      scales[0] = *reinterpret_cast<const uint32_t*>(s);
+    } else if constexpr (D == 128) {
+      const u32x2 v = *reinterpret_cast<const u32x2*>(s);
+      scales[0] = v.x;
+      scales[1] = v.y;
+    } else {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(s);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) scales[i] = v[i];
+    }
+  }
+  // Keys of tile j (tokens 16 j ..), the eight positions 8 step .. of the lane's quarter.
+  __device__ __forceinline__ f16x8 frag(int j, int step) const {
+    const int w = j * (D / 32) + step, b = j * (D / 64) + step / 2;
+    const uint32_t sw = scales[b / 4];
+    const f16x2 pair = (b % 4) / 2 ? e4m3x2<true>(sw) : e4m3x2<false>(sw);
+    const _Float16 s = pair[b % 2];
+    return e2m1x8(codes[w / 4][w % 4]) * f16x8{s, s, s, s, s, s, s, s};
+  }
+};
+
+__device__ __forceinline__ uint32_t bits_of(uint32_t mask, uint32_t a, uint32_t b) { return (a & mask) | (b & ~mask); }
+
+template <int D>
+struct VRegs {
+  u32x4 codes[D / 32];
+  uint32_t scales[4];  // byte i of scales[j]: token 16 j + 4 g + i
+  __device__ __forceinline__ void load(const uint8_t* block, int lane) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) codes[i] = load16(block + KvBlock<D>::kVCodes + i * 1024 + lane * 16);
+    const int g = lane >> 4, c = lane & 15;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(block + KvBlock<D>::kVScales + (c * (D / 16) / 16) * 64 + g * 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) scales[i] = v[i];
+  }
+  // Codes of a pair of tokens (2 p, 2 p + 1 of the lane's four of tile j) at
+  // eight positions (D == 64: four), one byte per position with the first
+  // token's code in its low nibble: even positions in .x, odd ones in .y.
+  __device__ __forceinline__ u32x2 pair(int j, int p, int half) const {
+    constexpr uint32_t kLow = 0x0F0F0F0Fu;
+    if constexpr (D == 64) {
+      const uint32_t w = codes[(j * 2 + p) / 4][(j * 2 + p) % 4];
+      return u32x2{bits_of(kLow, w, w >> 12), bits_of(kLow, w >> 4, w >> 16)};
+    } else {
+      const int i = (j * 4 + p * 2) * (D / 128) + half, i2 = i + D / 128;
+      const uint32_t a = codes[i / 4][i % 4], b = codes[i2 / 4][i2 % 4];
+      return u32x2{bits_of(kLow, a, b << 4), bits_of(kLow, a >> 4, b)};
+    }
+  }
+};
+
+template <int B>
+__device__ __forceinline__ f16x2 e2m1_at(u32x2 pair, int odd) {
+  return e2m1x2<B>(odd ? pair.y : pair.x);
+}
+__device__ __forceinline__ f16x2 e2m1_pos(u32x2 pair, int s) {  // position s (0 .. 7), a constant after unrolling
+  switch (s / 2) {
+    case 0: return e2m1_at<0>(pair, s & 1);
+    case 1: return e2m1_at<1>(pair, s & 1);
+    case 2: return e2m1_at<2>(pair, s & 1);
+    default: return e2m1_at<3>(pair, s & 1);
+  }
+}
+
+// Slots past the sequence's length hold anything: their V scales become 0, so
+// that the codes stand for 0 and not for NaN.  A NaN in a slot that only later
+// rows see must not reach the others through a weight of 0: such scales become
+// 0 too, and the rows that do see the slot are made NaN by hand.
+template <int D, int MT>
+__device__ __forceinline__ void clean_values(VRegs<D>& v, int first, int len, int lane, const int (&limit)[MT],
+                                             f32x4 (&o)[MT][D / 16]) {
+  const int g = lane >> 4;
+  uint32_t bad = 0u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    int left = len - (first + 16 * j + 4 * g);
+    left = left < 0 ? 0 : left;
+    if (left < 4) v.scales[j] &= (1u << (8 * left)) - 1u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (((v.scales[j] >> (8 * i)) & 0x7Fu) == 0x7Fu) {
+        bad |= 1u << (4 * j + i);
+        v.scales[j] &= ~(0xFFu << (8 * i));
+      }
+  }
+  if (!__any(bad != 0u)) return;
+#pragma unroll
+  for (int s = 1; s < 16; s <<= 1) bad |= __shfl_xor(bad, s);  // over the lanes of the same four tokens
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    bool seen = false;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      seen |= ((bad >> i) & 1u) && first + 16 * (i / 4) + 4 * g + i % 4 < limit[mt];
+    // Lanes of one query hold different positions: all four rows of lanes.
+    if (max_over_rows(seen ? 1.0f : 0.0f) > 0.0f) {
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s) o[mt][s] = f32x4{NAN, NAN, NAN, NAN};
+    }
+  }
+}
+
+template <int D, int MT, class E>
+__global__ __launch_bounds__(kThreads) void attend(const AttendArgs a) {
+  constexpr int DB = D / 16;
+  constexpr int kRow = D + 8;
+  __shared__ __align__(16) _Float16 qs[MT * 16 * kRow];
+  __shared__ float factor[MT * 16];
+  __shared__ float stat[kWaves][MT * 16][2];
+  __shared__ __align__(16) float sums[kWaves][D * 16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+  int i = blockIdx.x;
+  const int split = i % a.splits;
+  const int segment = i / a.splits;
+  i = segment;
+  const int qg = i % a.QG;
+  i /= a.QG;
+  const int h = i % a.c.Hk, b = i / a.c.Hk;
+  const int len = kv_len(a.c, b);
+  const int R = a.T * a.G;
+  stage_queries<D, MT, E>(a.q, b, h, qg, a.G, R, qs, factor);
+  __syncthreads();
+
+  int limit[MT];
+  float cm[MT], m[MT], msub[MT], l[MT];
+  f32x4 o[MT][DB];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int r = (qg * MT + mt) * 16 + c;
+    limit[mt] = r < R ? len - (a.T - 1 - r / a.G) : 0;
+    cm[mt] = fmaxf(a.scale * a.c.gk * kLog2e * factor[mt * 16 + c], kMinNormal);
+    m[mt] = -INFINITY;
+    msub[mt] = 0.0f;
+    l[mt] = 0.0f;
+#pragma unroll
+    for (int s = 0; s < DB; ++s) o[mt][s] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+
+  const int pages = (len + kPage - 1) / kPage, per = (pages + a.splits - 1) / a.splits;
+  const int p0 = split * per, p1 = p0 + per < pages ? p0 + per : pages;
+  const int32_t* table = a.c.table + static_cast<size_t>(b) * a.c.width;
+  for (int page = p0 + wave; page < p1; page += kWaves) {
+    const uint8_t* block = kv_block<D>(a.c, __builtin_amdgcn_readfirstlane(table[page]), h);
+    if (!block) continue;
+    const int first = page * kPage;
+    KRegs<D> k;
+    VRegs<D> v;
+    k.load(block, lane);
+    v.load(block, lane);
+    f32x4 s[4][MT];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) s[j][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int step = 0; step < D / 32; ++step) {
+      f16x8 qf[MT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        qf[mt] = *reinterpret_cast<const f16x8*>(qs + (mt * 16 + c) * kRow + g * (D / 4) + step * 8);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f16x8 kf = k.frag(j, step);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) s[j][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[mt], s[j][mt], 0, 0, 0);
+      }
+    }
+    if (first + kPage > len - (a.T - 1)) {  // some row does not see the whole page
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (first + 16 * j + 4 * g + e >= limit[mt]) s[j][mt][e] = -INFINITY;
+      clean_values<D, MT>(v, first, len, lane, limit, o);
+    }
+    bool grow = false;
+    float top[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      float t = s[0][mt][0];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t = fmaxf(t, s[j][mt][e]);
+      top[mt] = max_over_rows(t) * cm[mt];
+      grow |= top[mt] > m[mt] + kSlack;
+    }
+    if (__any(grow)) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const bool up = top[mt] > m[mt] + kSlack;
+        const float to = up ? top[mt] : m[mt];
+        const float alpha = up ? __builtin_amdgcn_exp2f(m[mt] - to) : 1.0f;
+        m[mt] = to;
+        msub[mt] = to == -INFINITY ? 0.0f : to - kLift;
+        l[mt] *= alpha;
+#pragma unroll
+        for (int d = 0; d < DB; ++d) o[mt][d] *= alpha;
+      }
+    }
+    f16x8 p[2][MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][mt][e], cm[mt], -msub[mt]));
+          l[mt] += w;
+          p[j / 2][mt][(j % 2) * 4 + e] = static_cast<_Float16>(w);
+        }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      f16x2 vs[4];  // scales of the token pairs: tile 2u tokens (0, 1), (2, 3), tile 2u + 1 the same
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        vs[2 * t] = e4m3x2<false>(v.scales[2 * u + t]);
+        vs[2 * t + 1] = e4m3x2<true>(v.scales[2 * u + t]);
+      }
+#pragma unroll
+      for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
+        u32x2 pr[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) pr[t] = v.pair(2 * u + t / 2, t % 2, half);
+#pragma unroll
+        for (int d = 0; d < (D == 64 ? 4 : 8); ++d) {
+          f16x8 vf;
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const f16x2 x = e2m1_pos(pr[t], d) * vs[t];
+            vf[2 * t] = x.x;
+            vf[2 * t + 1] = x.y;
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            o[mt][half * 8 + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p[u][mt], o[mt][half * 8 + d], 0, 0, 0);
+        }
+      }
+    }
+  }
+
+  // The wavefronts' sums meet in LDS, one group of 16 queries at a time.
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const float total = sum_over_rows(l[mt]);
+    if (g == 0) {
+      stat[wave][mt * 16 + c][0] = m[mt];
+      stat[wave][mt * 16 + c][1] = total;
+    }
+  }
+  for (int mt = 0; mt < MT; ++mt) {
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < MT; ++k)
+      if (k == mt) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+          *reinterpret_cast<f32x4*>(&sums[wave][(d * 16 + c) * 16 + 4 * g]) = o[k][d];
+      }
+    __syncthreads();
+    const int row = threadIdx.x / 16, at = threadIdx.x % 16;  // query, and the positions at * DB ..
+    const int local = mt * 16 + row, r = qg * MT * 16 + local;
+    if (r < R) {
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, stat[w][local][0]);
+      float f[kWaves], total = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        f[w] = mm == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(stat[w][local][0] - mm);
+        total += f[w] * stat[w][local][1];
+      }
+      const int t = r / a.G;
+      const size_t at_row = (static_cast<size_t>(b) * a.T + t) * a.Hq + h * a.G + r % a.G;
+      const size_t at_part = (static_cast<size_t>(blockIdx.x) * MT * 16 + local);
+      const float inv = a.splits > 1 ? 1.0f : (mm == -INFINITY ? 0.0f : a.c.gv / total);
+      float x[DB];
+#pragma unroll
+      for (int d = 0; d < DB; ++d) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) v += f[w] * sums[w][(d * 16 + row) * 16 + at];
+        x[d] = v * inv;
+      }
+      if (a.splits > 1) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d) a.part[at_part * D + at * DB + d] = x[d];
+        if (at == 0) {
+          a.stat[at_part * 2] = mm;
+          a.stat[at_part * 2 + 1] = total;
+        }
+      } else {
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at_row * D + at * DB);
+#pragma unroll
+        for (int d = 0; d < DB; d += 2) dst[d / 2] = elem_pack<E>(x[d], x[d + 1]);
+        if (at == 0 && a.lse)
+          a.lse[at_row] = mm == -INFINITY ? -INFINITY : (mm - kLift + __builtin_amdgcn_logf(total)) * kLn2;
+      }
+    }
+  }
+}
+
+// Adds the splits of a segment's 16 query rows.
+template <int D, int MT, class E>
+__global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a) {
+  constexpr int DB = D / 16;
+  const int mt = blockIdx.x % MT, segment = blockIdx.x / MT;
+  int i = segment;
+  const int qg = i % a.QG;
+  i /= a.QG;
+  const int h = i % a.c.Hk, b = i / a.c.Hk;
+  const int row = threadIdx.x / 16, at = threadIdx.x % 16;
+  const int local = mt * 16 + row, r = qg * MT * 16 + local;
+  if (r >= a.T * a.G) return;
+  const size_t base = static_cast<size_t>(segment) * a.splits * MT * 16 + local;
+  float mm = -INFINITY;
+  for (int s = 0; s < a.splits; ++s) mm = fmaxf(mm, a.stat[(base + static_cast<size_t>(s) * MT * 16) * 2]);
+  float x[DB], total = 0.0f;
+#pragma unroll
+  for (int d = 0; d < DB; ++d) x[d] = 0.0f;
+  for (int s = 0; s < a.splits; ++s) {
+    const size_t at_part = base + static_cast<size_t>(s) * MT * 16;
+    const float ms = a.stat[at_part * 2];
+    if (ms == -INFINITY) continue;
+    const float f = __builtin_amdgcn_exp2f(ms - mm);
+    total += f * a.stat[at_part * 2 + 1];
+#pragma unroll
+    for (int d = 0; d < DB; ++d) x[d] += f * a.part[at_part * D + at * DB + d];
+  }
+  const size_t at_row = (static_cast<size_t>(b) * a.T + r / a.G) * a.Hq + h * a.G + r % a.G;
+  const float inv = mm == -INFINITY ? 0.0f : a.c.gv / total;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at_row * D + at * DB);
+#pragma unroll
+  for (int d = 0; d < DB; d += 2) dst[d / 2] = elem_pack<E>(x[d] * inv, x[d + 1] * inv);
+  if (at == 0 && a.lse)
+    a.lse[at_row] = mm == -INFINITY ? -INFINITY : (mm - kLift + __builtin_amdgcn_logf(total)) * kLn2;
+}
+
+// ---- weights ----------------------------------------------------------------
+// The scores again, from the keys alone, in the other orientation (queries as
+// rows of the result): a lane's column is its token, and the sum over a head's
+// rows is a sum of its own values and of four lanes.
+struct WeightArgs {
+  kv4_cache c;
+  kv4_rows q;
+  const float* lse;
+  const float* acc;
+  float* out;
+  int T, Hq, G, per;  // per: pages per workgroup
+  float scale;
+};
+
+template <int D, int MT, class E>
+__global__ __launch_bounds__(kThreads) void add_weights(const WeightArgs a) {
+  constexpr int kRow = D + 8;
+  __shared__ __align__(16) _Float16 qs[MT * 16 * kRow];
+  __shared__ float factor[MT * 16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+  const int groups = (a.c.width + a.per - 1) / a.per;
+  int i = blockIdx.x;
+  const int chunk = i % groups;
+  i /= groups;
+  const int h = i % a.c.Hk, b = i / a.c.Hk;
+  const int len = kv_len(a.c, b), R = a.T * a.G;
+  const int p0 = chunk * a.per, p1 = p0 + a.per < a.c.width ? p0 + a.per : a.c.width;
+  const float* acc = a.acc + (static_cast<size_t>(b) * a.c.Hk + h) * a.c.width * kPage;
+  float* out = a.out + (static_cast<size_t>(b) * a.c.Hk + h) * a.c.width * kPage;
+  const int32_t* table = a.c.table + static_cast<size_t>(b) * a.c.width;
+  // Rows in groups of MT * 16; the first group also brings acc along.
+  for (int qg = 0; qg * MT * 16 < R; ++qg) {
+    __syncthreads();
+    if (p0 * kPage < len) stage_queries<D, MT, E>(a.q, b, h, qg, a.G, R, qs, factor);
+    __syncthreads();
+    float cm[MT][4], sub[MT][4];
+    int limit[MT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int local = mt * 16 + 4 * g + e, r = qg * MT * 16 + local;
+        limit[mt][e] = r < R ? len - (a.T - 1 - r / a.G) : 0;
+        cm[mt][e] = fmaxf(a.scale * a.c.gk * kLog2e * factor[local], kMinNormal);
+        sub[mt][e] = r < R ? a.lse[(static_cast<size_t>(b) * a.T + r / a.G) * a.Hq + h * a.G + r % a.G] * kLog2e : 0.0f;
+      }
+    for (int page = p0 + wave; page < p1; page += kWaves) {
+      const int first = page * kPage, slot = first + lane;
+      float sum = slot < len ? (qg == 0 ? acc[slot] : out[slot]) : 0.0f;
+      const uint8_t* block =
+          first < len ? kv_block<D>(a.c, __builtin_amdgcn_readfirstlane(table[page]), h) : nullptr;
+      if (block) {
+        KRegs<D> k;
+        k.load(block, lane);
+        f32x4 s[4][MT];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) s[j][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int step = 0; step < D / 32; ++step) {
+          f16x8 qf[MT];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            qf[mt] = *reinterpret_cast<const f16x8*>(qs + (mt * 16 + c) * kRow + g * (D / 4) + step * 8);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const f16x8 kf = k.frag(j, step);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              s[j][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qf[mt], kf, s[j][mt], 0, 0, 0);
+          }
+        }
+        float mine = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float w = 0.0f;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][mt][e], cm[mt][e], -sub[mt][e]));
+              w += first + 16 * j + c < limit[mt][e] ? p : 0.0f;
+            }
+          w = sum_over_rows(w);
+          mine = j == g ? w : mine;  // lane 16 g + c keeps token 16 g + c
+        }
+        if (slot < len) sum += mine;
+      }
+      out[slot] = sum;
+    }
+  }
+}
+
+// Most tiles of 16 query rows that a wavefront's registers hold: a tile takes
+// D / 4 of them for its sums and 16 for a page's scores.
+constexpr int max_tiles(int D) { return D == 256 ? 2 : 3; }
+
+template <int D, class F>
+void by_tiles(int tiles, F f) {
+  if (tiles == 1) f(std::integral_constant<int, 1>());
+  else if (tiles == 2) f(std::integral_constant<int, 2>());
+  else if constexpr (max_tiles(D) > 2) f(std::integral_constant<int, 3>());
+}
+
+template <class F>
+hipError_t by_shape(int D, int type, int tiles, F f) {
+  const auto run = [&](auto d) {
+    by_tiles<d()>(tiles, [&](auto mt) {
+      if (type == SKINNY_F16) f(d, mt, F16());
+      else f(d, mt, BF16());
+    });
+  };
+  if (D == 64) run(std::integral_constant<int, 64>());
+  else if (D == 128) run(std::integral_constant<int, 128>());
+  else run(std::integral_constant<int, 256>());
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// Query rows of a head go in the fewest groups of at most max_tiles(D) tiles, of equal size.
+AttendPlan kv4_attend_plan(int B, int T, int Hq, int Hk, int D, int width) {
+  AttendPlan p;
+  const int tiles = (T * (Hq / Hk) + 15) / 16;
+  p.QG = (tiles + max_tiles(D) - 1) / max_tiles(D);
+  p.MT = (tiles + p.QG - 1) / p.QG;
+  const int64_t segments = static_cast<int64_t>(B) * Hk * p.QG;
+  int64_t splits = 1024 / segments;
+  const int most = (width + kWaves - 1) / kWaves;
+  splits = splits < 1 ? 1 : (splits > most ? most : splits);
+  p.splits = static_cast<int>(splits);
+  const size_t rows = static_cast<size_t>(segments) * p.splits * p.MT * 16;
+  p.part_off = kSyncBytes;
+  p.stat_off = p.part_off + rows * D * 4;
+  p.total = p.splits > 1 ? p.stat_off + rows * 8 : 0;
+  return p;
+}
+
+hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type, int T, int Hq, float scale, void* out,
+                                float* lse, void* workspace, hipStream_t stream) {
+  const AttendPlan p = kv4_attend_plan(c.B, T, Hq, c.Hk, c.D, c.width);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  AttendArgs a{c, q, out, lse, nullptr, nullptr, T, Hq, Hq / c.Hk, p.QG, p.splits, scale};
+  if (p.splits > 1) {
+    a.part = reinterpret_cast<float*>(ws + p.part_off);
+    a.stat = reinterpret_cast<float*>(ws + p.stat_off);
+  }
+  const unsigned segments = static_cast<unsigned>(c.B * c.Hk * p.QG);
+  return by_shape(c.D, type, p.MT, [&](auto d, auto mt, auto e) {
+    attend<d(), mt(), decltype(e)><<<dim3(segments * p.splits), kThreads, 0, stream>>>(a);
+    if (p.splits > 1) attend_join<d(), mt(), decltype(e)><<<dim3(segments * mt()), kThreads, 0, stream>>>(a);
+  });
+}
+
+hipError_t launch_kv4_weights(const kv4_cache& c, const kv4_rows& q, int type, int T, int Hq, float scale,
+                              const float* lse, const float* acc, float* acc_out, hipStream_t stream) {
+  const int G = Hq / c.Hk, all = (T * G + 15) / 16, tiles = all < max_tiles(c.D) ? all : max_tiles(c.D);
+  const int64_t pages = static_cast<int64_t>(c.B) * c.Hk * c.width;
+  int64_t per = pages / 1024;
+  per = per < kWaves ? kWaves : (per > 16 ? 16 : per);
+  WeightArgs a{c, q, lse, acc, acc_out, T, Hq, G, static_cast<int>(per), scale};
+  const int64_t groups = (c.width + per - 1) / per;
+  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(c.B) * c.Hk * groups));
+  return by_shape(c.D, type, tiles, [&](auto d, auto mt, auto e) {
+    add_weights<d(), mt(), decltype(e)><<<grid, kThreads, 0, stream>>>(a);
+  });
+}
+
+}  // namespace skinny

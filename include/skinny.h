@@ -459,6 +459,165 @@ int skinny_read_probe_pattern(const void* buf, size_t bytes, int pattern,
                               int a, int b, uint32_t* sink, size_t* bytes_read,
                               hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The 4-bit key/value cache.
+ *
+ * Keys and values are held in NVFP4: E2M1 codes, one E4M3FN scale per 16
+ * consecutive values of a head, and an fp32 scale per tensor (gk for the keys,
+ * gv for the values); a held value is e2m1(code) * e4m3(scale) * g.
+ *
+ * The cache is an array of pages of SKINNY_KV_PAGE = 64 tokens.  A page holds,
+ * for each of the Hk key/value heads, a block of 72 * D bytes (D: the head
+ * size, 64, 128 or 256): K codes (32 D), K scales (4 D), V codes (32 D), V
+ * scales (4 D).  For token t (0 .. 63) of the page and position d of the head:
+ *   K code : q = d / (D/4), i = d % (D/4), run = (t/16) * (D/8) + i/2;
+ *            byte (run/16) * 1024 + q * 256 + (t%16) * 16 + run%16,
+ *            the low nibble for even d.
+ *   K scale: byte 32 D + (q * 16 + t%16) * (D/16) + (t/16) * (D/64) + i/16.
+ *   V code : c = d / (D/16), i = d % (D/16), o = (t/16) * 4 + t%4,
+ *            run = o * (D/32) + i/2; byte 36 D + (run/16) * 1024 +
+ *            ((t%16)/4) * 256 + c * 16 + run%16, the low nibble for even d.
+ *   V scale: byte 68 D + (d/16) * 64 + ((t%16)/4) * 16 + o.
+ * These orders are the register layouts of the attention's matrix products:
+ * every 16-byte load of a wavefront is contiguous with its neighbours', and
+ * each lane finds its own tokens' codes and scales in it.
+ *
+ *   data   : device, [pages][Hk][72 * D] bytes.
+ *   table  : device, int32 [B][width]: the pages of each sequence, in order.
+ *            Slot s of a sequence is token s % 64 of page table[b][s / 64].
+ *   lens   : device, int32 [B]: the slots of each sequence, this step's own
+ *            tokens among them.  A value below 0 counts as 0 and one past
+ *            64 * width as that.
+ *   pages  : pages in data, 1 .. 2^31 - 1;  width >= 1;  1 <= B <= 65536;
+ *            1 <= Hk <= 1024;  64 * width < 2^31.
+ *   gk, gv : finite and > 0.
+ *
+ * A table entry outside 0 .. pages - 1 that a sequence's slots reach names no
+ * page: nothing is read or written there, its slots are held by nobody
+ * (attention and its weights skip them, reads and evictions give zeros).
+ *
+ * Rows: a step's T rows per sequence are right-aligned: row t stands for slot
+ * lens - T + t; a row whose slot is negative has no token.  q, k and v are
+ * given by kv4_rows: a device pointer and the strides, in elements, of the
+ * sequence, the row and the head (0 where that dimension has one entry and
+ * never otherwise negative); the D values of a head are contiguous.  The
+ * pointer is 16-byte aligned and the strides are multiples of 8 elements, so
+ * that views of a qkv GEMM's output serve as they are.
+ *
+ * type: the elements of q, k, v and of the outputs: SKINNY_F16 or SKINNY_BF16.
+ * ------------------------------------------------------------------------- */
+enum { SKINNY_F16 = 0, SKINNY_BF16 = 1, SKINNY_F32 = 2 };
+#define SKINNY_KV_PAGE 64
+#define SKINNY_KV_MAX_GROUP 64   /* query heads per key/value head */
+
+typedef struct kv4_cache {
+  void* data;
+  const int32_t* table;
+  const int32_t* lens;
+  int32_t pages, width, B, Hk, D;
+  float gk, gv;
+} kv4_cache;
+
+typedef struct kv4_rows {
+  const void* data;
+  int64_t sequence, row, head;
+} kv4_rows;
+
+/* kv4_append -- writes the newest T slots of every sequence.  Per 16 values of
+ * a head: scale = E4M3(min(amax / (6 g), 448)), code = E2M1(x / (scale * g)),
+ * both to the nearest, ties to even, saturating, decided without rounding
+ * before (the sign of zero is kept; codes are 0 where the scale is).  A group
+ * with an infinity saturates; a group with a NaN is held as NaN.  Rows without
+ * a token are dropped.  T >= 1.  Other bytes of the pages are left alone.  Two
+ * sequences must not append to one page in the same call. */
+int kv4_append(const kv4_cache* cache, const kv4_rows* k, const kv4_rows* v,
+               int type, int T, hipStream_t stream);
+
+/* kv4_read -- the newest n slots as held: k and v, device [B][n][Hk][D] of
+ * `type`, row t = slot lens - n + t, zeros where that is negative. */
+int kv4_read(const kv4_cache* cache, void* k, void* v, int type, int n,
+             hipStream_t stream);
+
+/* kv4_attention -- out = softmax(scale * q . K~) . V~ over the cache, row t of
+ * a sequence over its first lens - (T - 1 - t) slots (causal among the step's
+ * own rows), Hq query heads sharing Hk key/value heads in order (Hq a multiple
+ * of Hk, at most SKINNY_KV_MAX_GROUP of them per head).
+ *   q    : [B][T][Hq][D] by strides;  1 <= T <= SKINNY_MAX_M.
+ *   out  : device [B][T][Hq][D] of `type`, contiguous; zeros for a row that
+ *          sees no slot.
+ *   lse  : device fp32 [B][T][Hq] or NULL: log(sum(exp(scale * q . K~))), -inf
+ *          for a row that sees no slot.
+ *   workspace : kv4_attention_workspace_bytes(B, T, Hq, Hk, D, width) bytes
+ *          (see "Workspaces").
+ * Scores, the softmax and the sums are fp32; the weights of V~ are rounded to
+ * fp16, relative to the row's greatest.  bf16 queries are scaled to fp16's
+ * range by a power of two per row, which changes no value above 2^-39 of the
+ * row's greatest.  A NaN among the values of a slot that only some rows see
+ * makes those rows NaN and no others. */
+int kv4_attention(const kv4_cache* cache, const kv4_rows* q, int type, int T,
+                  int Hq, float scale, void* out, float* lse, void* workspace,
+                  size_t workspace_bytes, hipStream_t stream);
+size_t kv4_attention_workspace_bytes(int B, int T, int Hq, int Hk, int D,
+                                     int width);
+
+/* kv4_attention_weights -- adds the attention weights of a step to the slots:
+ * acc_out[b][h][s] = acc[b][h][s] + sum over the rows and query heads of h that
+ * see slot s of exp(scale * q . k~_s - lse).  Slots past lens get 0.
+ *   q, T, Hq, scale, type : as for kv4_attention;  lse: its output.
+ *   acc, acc_out : device fp32 [B][Hk][64 * width], 16-byte aligned; they may
+ *          be the same buffer.
+ * gv and the values are not used. */
+int kv4_attention_weights(const kv4_cache* cache, const kv4_rows* q, int type,
+                          int T, int Hq, float scale, const float* lse,
+                          const float* acc, float* acc_out, hipStream_t stream);
+
+/* kv4_evict -- copies the slots worth keeping into other pages.  Per sequence
+ * and head the `keep` slots with the greatest accumulated weight stay, in
+ * their order; the first `sinks` and the last `recent` slots always do; of
+ * equal weights the lower slot stays.  A sequence of at most `keep` slots
+ * keeps all of them.  Codes and scales are copied as they are.
+ *   acc       : device fp32 [B][Hk][64 * cache->width] (weights are >= 0; a NaN
+ *               counts as the least).
+ *   dst       : the pages to write, another table and another array than
+ *               cache's (dst->lens is not used and may be NULL); B, Hk and D as in cache;
+ *               64 * dst->width >= keep.  Slots past the new length in a
+ *               sequence's last page are set to zero bytes.
+ *   kept      : device int32 [B][Hk][keep]: the slots kept, -1 past them.
+ *   new_lens  : device int32 [B]: min(lens, keep).
+ *   new_acc   : device fp32 [B][Hk][64 * dst->width]: their weights, 0 past them.
+ *   1 <= keep;  0 <= sinks, recent;  sinks + recent <= keep. */
+int kv4_evict(const kv4_cache* cache, const float* acc, const kv4_cache* dst,
+              int32_t* kept, int32_t* new_lens, float* new_acc, int keep,
+              int sinks, int recent, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * lm_head_logprobs -- log probabilities from an lm_head's logits, one pass.
+ *
+ * With lse = log(sum_i exp(x[r][i])):
+ *   logits    : device [R][V] of `type` (SKINNY_F16, SKINNY_BF16 or
+ *               SKINNY_F32), rows `stride` elements apart (stride >= V).
+ *   tokens    : device int32 [R].
+ *   logprob   : device fp32 [R]: x[r][tokens[r]] - lse; NaN for a token
+ *               outside 0 .. V-1.
+ *   entropy   : device fp32 [R]: -sum_i p_i log p_i, p = exp(x - lse).
+ *   top_ids   : device int32 [R][k]: the k greatest logits in falling order,
+ *               ties to the lower index; 1 <= k <= SKINNY_MAX_TOP, k <= V.
+ *   top_logprobs : device fp32 [R][k]: their log probabilities.
+ *   workspace : lm_head_logprobs_workspace_bytes(R, V, k) bytes (see
+ *               "Workspaces"; may be NULL when that is 0).
+ * 1 <= R < 2^24, 1 <= V <= 2^24.  A row whose logits are all -inf has log
+ * probabilities of -inf and entropy 0.  A NaN makes its row's logprob, entropy
+ * and top_logprobs NaN and is never among top_ids (-1 where fewer than k
+ * logits are numbers).  Every sum is fp32 or wider.
+ * ------------------------------------------------------------------------- */
+#define SKINNY_MAX_TOP 32
+int lm_head_logprobs(const void* logits, int type, int64_t stride,
+                     const int32_t* tokens, float* logprob, float* entropy,
+                     int32_t* top_ids, float* top_logprobs, int R, int V, int k,
+                     void* workspace, size_t workspace_bytes,
+                     hipStream_t stream);
+size_t lm_head_logprobs_workspace_bytes(int R, int V, int k);
+
 /* Static description of a status code (never NULL). */
 const char* skinny_strerror(int status);
 
