@@ -222,10 +222,13 @@ hipError_t launch_kv4_read(const kv4_cache& c, uint16_t* k, uint16_t* v, int typ
 hipError_t launch_kv4_evict(const kv4_cache& c, const float* acc, const kv4_cache& dst, int32_t* kept,
                             int32_t* new_lens, float* new_acc, int keep, int sinks, int recent, hipStream_t stream);
 // How an attention call is laid out: query tiles of 16 rows per workgroup and
-// groups of them per head, splits of a sequence, and its workspace.
+// groups of them per head, fewest pages of a workgroup, whether segments may be
+// split, the grid, and the workspace.
 struct AttendPlan {
-  int MT, QG, splits;
-  size_t part_off, stat_off, total;
+  int MT, QG, least;
+  bool split;
+  int64_t grid;
+  size_t split_off, stat_off, part_off, total;
 };
 AttendPlan kv4_attend_plan(int B, int T, int Hq, int Hk, int D, int width);
 hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type, int T, int Hq, float scale, void* out,

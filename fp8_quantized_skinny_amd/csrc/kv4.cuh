@@ -81,9 +81,22 @@ __device__ __forceinline__ int kv_scale_at(int t, int f, bool v) {
   return v ? KvBlock<D>::v_scale(t, f) : KvBlock<D>::k_scale(t, f);
 }
 
+// p[i] for an i that is one for the whole wavefront, through the scalar cache:
+// no register of the lanes, and no wait for the vector loads in flight.  For
+// what nothing writes while the kernel runs (tables and lengths).
+__device__ __forceinline__ int uniform_load(const int32_t* p, int64_t i) {
+  typedef const __attribute__((address_space(4))) int32_t* Constant;
+  return reinterpret_cast<Constant>(reinterpret_cast<uintptr_t>(p))[i];
+}
+
 // The slots of sequence b, within what its table holds.
 __device__ __forceinline__ int kv_len(const kv4_cache& c, int b) {
   const int n = c.lens[b];
+  return n < 0 ? 0 : (n > c.width * kPage ? c.width * kPage : n);
+}
+
+__device__ __forceinline__ int kv_len_uniform(const kv4_cache& c, int b) {
+  const int n = uniform_load(c.lens, b);
   return n < 0 ? 0 : (n > c.width * kPage ? c.width * kPage : n);
 }
 

@@ -41,9 +41,11 @@ struct AttendArgs {
   kv4_rows q;
   void* out;
   float* lse;
-  float* part;  // [segment * splits + split][MT * 16][D] sums, then the statistics
-  float* stat;  // [segment * splits + split][MT * 16][2]: reference maximum (log2), sum
-  int T, Hq, G, QG, splits;
+  float* part;   // [share][MT * 16][D]: sums of a split segment's shares
+  float* stat;   // [share][MT * 16][2]: their reference maximum (log2) and sum
+  int2* split;   // [segment]: its first share and their number
+  int T, Hq, G, QG;
+  int least;     // fewest pages of a share
   float scale;
 };
 
@@ -206,53 +208,149 @@ __device__ __forceinline__ void clean_values(VRegs<D>& v, int first, int len, in
   }
 }
 
+// Inclusive sums over the lanes of a wavefront (DPP row shifts and broadcasts).
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);   // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);   // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);   // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31
+  return v;
+}
+
+// A workgroup's share of the work: pages p0 .. p1 of one segment (sequence b,
+// head h, query group qg).  The lengths are known to the device only, so every
+// wavefront works the same plan out of them: the least number of pages per
+// share for which the shares of all segments, each cut into equal ones, fit
+// the grid.  A long sequence among short ones then has more workgroups, and no
+// share is much longer than the mean.
+struct Share {
+  int b, h, qg, len, p0, p1, splits, first;  // first: the segment's first share; the next is Hk * QG further
+  bool any;
+};
+__device__ __forceinline__ Share plan_share(const kv4_cache& c, int QG, int least, int lane) {
+  const int per = c.Hk * QG;                      // segments of a sequence
+  const int room = static_cast<int>(gridDim.x) / per;  // shares per head and query group; at least B
+  const int at = static_cast<int>(blockIdx.x) / per;
+  Share s;
+  s.any = false;
+  s.b = s.len = s.p0 = s.p1 = s.splits = s.first = 0;
+  const int hq = static_cast<int>(blockIdx.x) % per;
+  s.h = hq / QG;
+  s.qg = hq % QG;
+  const auto pages = [&](int b) { return b < c.B ? (kv_len(c, b) + kPage - 1) / kPage : 0; };
+  int mine = pages(lane), total = 0;
+  for (int b0 = 0; b0 < c.B; b0 += 64)
+    total += __builtin_amdgcn_readlane(wave_scan(b0 ? pages(b0 + lane) : mine), 63);
+  int chunk = total / (room - (c.B >> 1)) + 1;
+  chunk = chunk < least ? least : chunk;
+  const auto shares = [&](int b0) {
+    const int n = ((b0 ? pages(b0 + lane) : mine) + chunk - 1) / chunk;
+    return b0 + lane < c.B ? (n < 1 ? 1 : n) : 0;
+  };
+  for (;;) {
+    int all = 0;
+    for (int b0 = 0; b0 < c.B; b0 += 64) all += __builtin_amdgcn_readlane(wave_scan(shares(b0)), 63);
+    if (all <= room) break;
+    chunk += (chunk >> 4) + 1;
+  }
+  int before = 0;
+  for (int b0 = 0; b0 < c.B; b0 += 64) {
+    const int n = shares(b0), upto = before + wave_scan(n);
+    const int last = __builtin_amdgcn_readlane(upto, 63);
+    if (at < last) {
+      const int l = __popcll(__ballot(upto <= at));  // the lane of the sequence
+      s.any = true;
+      s.b = b0 + l;
+      s.splits = __builtin_amdgcn_readlane(n, l);
+      const int first = __builtin_amdgcn_readlane(upto, l) - s.splits;
+      s.first = first * per + hq;
+      s.len = kv_len_uniform(c, s.b);
+      const int np = (s.len + kPage - 1) / kPage, each = (np + s.splits - 1) / s.splits;
+      s.p0 = (at - first) * each;
+      s.p1 = s.p0 + each < np ? s.p0 + each : np;
+      break;
+    }
+    before = last;
+  }
+  // The compiler does not see that all lanes agree.
+  for (int* f : {&s.b, &s.h, &s.qg, &s.len, &s.p0, &s.p1, &s.splits, &s.first}) *f = __builtin_amdgcn_readfirstlane(*f);
+  return s;
+}
+
+// A page that the table does not name is read as page 0 and lies past every limit.
+struct Page {
+  const uint8_t* block;
+  int first;
+};
+template <int D>
+__device__ __forceinline__ Page page_of(const kv4_cache& c, int id, int page, int h) {
+  const bool named = static_cast<unsigned>(id) < static_cast<unsigned>(c.pages);
+  return Page{static_cast<const uint8_t*>(c.data) +
+                  (static_cast<size_t>(named ? id : 0) * c.Hk + h) * KvBlock<D>::kBytes,
+              named ? page * kPage : 0x3FFFFFFF};
+}
+
+// Workgroups per CU that a wavefront's registers allow.
+constexpr int attend_per_cu(int D, int MT) { return D == 256 && MT == 2 ? 1 : (D / 64 * MT <= 2 ? 3 : 2); }
+
 template <int D, int MT, class E>
-__global__ __launch_bounds__(kThreads) void attend(const AttendArgs a) {
+__global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const AttendArgs a) {
   constexpr int DB = D / 16;
   constexpr int kRow = D + 8;
+  // With the most sums, keys that arrive during the softmax have no registers.
+  constexpr bool kLateKeys = D == 128 && MT == 3;
   __shared__ __align__(16) _Float16 qs[MT * 16 * kRow];
   __shared__ float factor[MT * 16];
+  __shared__ int limits[MT * 16];  // slots that each row sees
   __shared__ float stat[kWaves][MT * 16][2];
   __shared__ __align__(16) float sums[kWaves][D * 16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
-  int i = blockIdx.x;
-  const int split = i % a.splits;
-  const int segment = i / a.splits;
-  i = segment;
-  const int qg = i % a.QG;
-  i /= a.QG;
-  const int h = i % a.c.Hk, b = i / a.c.Hk;
-  const int len = kv_len(a.c, b);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, c = lane & 15;
+  const Share sh = plan_share(a.c, a.QG, a.least, lane);
+  if (!sh.any) return;
+  const int b = sh.b, h = sh.h, qg = sh.qg, len = sh.len;
   const int R = a.T * a.G;
+  if (a.split && sh.first == static_cast<int>(blockIdx.x) && threadIdx.x == 0)
+    a.split[(b * a.c.Hk + h) * a.QG + qg] = int2{sh.first, sh.splits};
+  const int32_t* table = a.c.table + static_cast<size_t>(b) * a.c.width;
+  int page = sh.p0 + wave;
+  KRegs<D> k;
+  VRegs<D> v;
+  Page now{nullptr, 0}, next{nullptr, 0};
+  int next_id = 0;
+  if (page < sh.p1) {
+    now = page_of<D>(a.c, uniform_load(table, page), page, h);
+    next_id = uniform_load(table, page + kWaves < sh.p1 ? page + kWaves : page);
+    k.load(now.block, lane);
+    v.load(now.block, lane);
+  }
   stage_queries<D, MT, E>(a.q, b, h, qg, a.G, R, qs, factor);
+  if (threadIdx.x < MT * 16) {
+    const int r = qg * MT * 16 + threadIdx.x;
+    limits[threadIdx.x] = r < R ? len - (a.T - 1 - r / a.G) : 0;
+  }
   __syncthreads();
 
-  int limit[MT];
-  float cm[MT], m[MT], msub[MT], l[MT];
+  float cm[MT], m[MT], l[MT];
   f32x4 o[MT][DB];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    const int r = (qg * MT + mt) * 16 + c;
-    limit[mt] = r < R ? len - (a.T - 1 - r / a.G) : 0;
     cm[mt] = fmaxf(a.scale * a.c.gk * kLog2e * factor[mt * 16 + c], kMinNormal);
     m[mt] = -INFINITY;
-    msub[mt] = 0.0f;
     l[mt] = 0.0f;
 #pragma unroll
     for (int s = 0; s < DB; ++s) o[mt][s] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  const int pages = (len + kPage - 1) / kPage, per = (pages + a.splits - 1) / a.splits;
-  const int p0 = split * per, p1 = p0 + per < pages ? p0 + per : pages;
-  const int32_t* table = a.c.table + static_cast<size_t>(b) * a.c.width;
-  for (int page = p0 + wave; page < p1; page += kWaves) {
-    const uint8_t* block = kv_block<D>(a.c, __builtin_amdgcn_readfirstlane(table[page]), h);
-    if (!block) continue;
-    const int first = page * kPage;
-    KRegs<D> k;
-    VRegs<D> v;
-    k.load(block, lane);
-    v.load(block, lane);
+  // The next page's keys are loaded once this page's have been used, and its
+  // values once this page's have: each load has the other product to arrive in,
+  // and no registers hold two pages.
+  for (; page < sh.p1; page += kWaves) {
+    const int first = now.first;
+    // Past the last page the prefetch reads this one again.
+    next = page + kWaves < sh.p1 ? page_of<D>(a.c, next_id, page + kWaves, h) : now;
+    next_id = uniform_load(table, page + 2 * kWaves < sh.p1 ? page + 2 * kWaves : page);
     f32x4 s[4][MT];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -270,8 +368,15 @@ __global__ __launch_bounds__(kThreads) void attend(const AttendArgs a) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) s[j][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[mt], s[j][mt], 0, 0, 0);
       }
+      // Without these fences the scheduler widens many steps' codes at once,
+      // and their registers cost the second wavefront of a SIMD.
+      __builtin_amdgcn_sched_barrier(0);
     }
+    if constexpr (!kLateKeys) k.load(next.block, lane);
     if (first + kPage > len - (a.T - 1)) {  // some row does not see the whole page
+      int limit[MT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) limit[mt] = limits[mt * 16 + c];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -300,7 +405,6 @@ __global__ __launch_bounds__(kThreads) void attend(const AttendArgs a) {
         const float to = up ? top[mt] : m[mt];
         const float alpha = up ? __builtin_amdgcn_exp2f(m[mt] - to) : 1.0f;
         m[mt] = to;
-        msub[mt] = to == -INFINITY ? 0.0f : to - kLift;
         l[mt] *= alpha;
 #pragma unroll
         for (int d = 0; d < DB; ++d) o[mt][d] *= alpha;
@@ -308,15 +412,19 @@ __global__ __launch_bounds__(kThreads) void attend(const AttendArgs a) {
     }
     f16x8 p[2][MT];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) {
+      const float lifted = m[mt] == -INFINITY ? 0.0f : m[mt] - kLift;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][mt][e], cm[mt], -msub[mt]));
+          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][mt][e], cm[mt], -lifted));
           l[mt] += w;
           p[j / 2][mt][(j % 2) * 4 + e] = static_cast<_Float16>(w);
         }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (kLateKeys) k.load(next.block, lane);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       f16x2 vs[4];  // scales of the token pairs: tile 2u tokens (0, 1), (2, 3), tile 2u + 1 the same
@@ -342,9 +450,12 @@ __global__ __launch_bounds__(kThreads) void attend(const AttendArgs a) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
             o[mt][half * 8 + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p[u][mt], o[mt][half * 8 + d], 0, 0, 0);
+          if (d % 2) __builtin_amdgcn_sched_barrier(0);
         }
       }
     }
+    v.load(next.block, lane);
+    now = next;
   }
 
   // The wavefronts' sums meet in LDS, one group of 16 queries at a time.
@@ -381,7 +492,7 @@ __global__ __launch_bounds__(kThreads) void attend(const AttendArgs a) {
       const int t = r / a.G;
       const size_t at_row = (static_cast<size_t>(b) * a.T + t) * a.Hq + h * a.G + r % a.G;
       const size_t at_part = (static_cast<size_t>(blockIdx.x) * MT * 16 + local);
-      const float inv = a.splits > 1 ? 1.0f : (mm == -INFINITY ? 0.0f : a.c.gv / total);
+      const float inv = sh.splits > 1 ? 1.0f : (mm == -INFINITY ? 0.0f : a.c.gv / total);
       float x[DB];
 #pragma unroll
       for (int d = 0; d < DB; ++d) {
@@ -390,7 +501,7 @@ __global__ __launch_bounds__(kThreads) void attend(const AttendArgs a) {
         for (int w = 0; w < kWaves; ++w) v += f[w] * sums[w][(d * 16 + row) * 16 + at];
         x[d] = v * inv;
       }
-      if (a.splits > 1) {
+      if (sh.splits > 1) {
 #pragma unroll
         for (int d = 0; d < DB; ++d) a.part[at_part * D + at * DB + d] = x[d];
         if (at == 0) {
@@ -408,38 +519,57 @@ __global__ __launch_bounds__(kThreads) void attend(const AttendArgs a) {
   }
 }
 
-// Adds the splits of a segment's 16 query rows.
+// Adds the shares of split segments: D / 4 threads per query row, each taking
+// four positions of every share, eight shares' loads at a time.
 template <int D, int MT, class E>
 __global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a) {
-  constexpr int DB = D / 16;
-  const int mt = blockIdx.x % MT, segment = blockIdx.x / MT;
+  constexpr int kPer = D / 4, kRows = kThreads / kPer, kBatch = 8;
+  constexpr int kGroups = MT * 16 / kRows;
+  const int segment = blockIdx.x / kGroups;
+  const int2 split = a.split[segment];
+  if (split.y <= 1) return;
   int i = segment;
   const int qg = i % a.QG;
   i /= a.QG;
-  const int h = i % a.c.Hk, b = i / a.c.Hk;
-  const int row = threadIdx.x / 16, at = threadIdx.x % 16;
-  const int local = mt * 16 + row, r = qg * MT * 16 + local;
+  const int h = i % a.c.Hk, b = i / a.c.Hk, stride = a.c.Hk * a.QG;
+  const int local = blockIdx.x % kGroups * kRows + threadIdx.x / kPer, at = threadIdx.x % kPer;
+  const int r = qg * MT * 16 + local;
   if (r >= a.T * a.G) return;
-  const size_t base = static_cast<size_t>(segment) * a.splits * MT * 16 + local;
-  float mm = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) mm = fmaxf(mm, a.stat[(base + static_cast<size_t>(s) * MT * 16) * 2]);
-  float x[DB], total = 0.0f;
+  const auto row = [&](int s) { return (static_cast<size_t>(split.x) + static_cast<size_t>(s) * stride) * (MT * 16) + local; };
+  float mm = -INFINITY, total = 0.0f;
+  f32x4 x{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s0 = 0; s0 < split.y; s0 += kBatch) {
+    float ms[kBatch], ls[kBatch];
+    f32x4 v[kBatch];
 #pragma unroll
-  for (int d = 0; d < DB; ++d) x[d] = 0.0f;
-  for (int s = 0; s < a.splits; ++s) {
-    const size_t at_part = base + static_cast<size_t>(s) * MT * 16;
-    const float ms = a.stat[at_part * 2];
-    if (ms == -INFINITY) continue;
-    const float f = __builtin_amdgcn_exp2f(ms - mm);
-    total += f * a.stat[at_part * 2 + 1];
+    for (int s = 0; s < kBatch; ++s) {
+      const bool in = s0 + s < split.y;
+      const size_t p = row(in ? s0 + s : s0);
+      const float2 st = *reinterpret_cast<const float2*>(a.stat + p * 2);
+      ms[s] = in ? st.x : -INFINITY;
+      ls[s] = st.y;
+      v[s] = *reinterpret_cast<const f32x4*>(a.part + p * D + at * 4);
+    }
+    float to = mm;
 #pragma unroll
-    for (int d = 0; d < DB; ++d) x[d] += f * a.part[at_part * D + at * DB + d];
+    for (int s = 0; s < kBatch; ++s) to = fmaxf(to, ms[s]);
+    if (to == -INFINITY) continue;
+    const float f0 = __builtin_amdgcn_exp2f(mm - to);
+    x *= f0;
+    total *= f0;
+    mm = to;
+#pragma unroll
+    for (int s = 0; s < kBatch; ++s) {
+      if (ms[s] == -INFINITY) continue;
+      const float f = __builtin_amdgcn_exp2f(ms[s] - mm);
+      total += f * ls[s];
+      x += f * v[s];
+    }
   }
   const size_t at_row = (static_cast<size_t>(b) * a.T + r / a.G) * a.Hq + h * a.G + r % a.G;
-  const float inv = mm == -INFINITY ? 0.0f : a.c.gv / total;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at_row * D + at * DB);
-#pragma unroll
-  for (int d = 0; d < DB; d += 2) dst[d / 2] = elem_pack<E>(x[d] * inv, x[d + 1] * inv);
+  x *= mm == -INFINITY ? 0.0f : a.c.gv / total;
+  *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at_row * D + at * 4) =
+      u32x2{elem_pack<E>(x[0], x[1]), elem_pack<E>(x[2], x[3])};
   if (at == 0 && a.lse)
     a.lse[at_row] = mm == -INFINITY ? -INFINITY : (mm - kLift + __builtin_amdgcn_logf(total)) * kLn2;
 }
@@ -463,13 +593,13 @@ __global__ __launch_bounds__(kThreads) void add_weights(const WeightArgs a) {
   constexpr int kRow = D + 8;
   __shared__ __align__(16) _Float16 qs[MT * 16 * kRow];
   __shared__ float factor[MT * 16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, c = lane & 15;
   const int groups = (a.c.width + a.per - 1) / a.per;
   int i = blockIdx.x;
   const int chunk = i % groups;
   i /= groups;
   const int h = i % a.c.Hk, b = i / a.c.Hk;
-  const int len = kv_len(a.c, b), R = a.T * a.G;
+  const int len = kv_len_uniform(a.c, b), R = a.T * a.G;
   const int p0 = chunk * a.per, p1 = p0 + a.per < a.c.width ? p0 + a.per : a.c.width;
   const float* acc = a.acc + (static_cast<size_t>(b) * a.c.Hk + h) * a.c.width * kPage;
   float* out = a.out + (static_cast<size_t>(b) * a.c.Hk + h) * a.c.width * kPage;
@@ -493,8 +623,7 @@ __global__ __launch_bounds__(kThreads) void add_weights(const WeightArgs a) {
     for (int page = p0 + wave; page < p1; page += kWaves) {
       const int first = page * kPage, slot = first + lane;
       float sum = slot < len ? (qg == 0 ? acc[slot] : out[slot]) : 0.0f;
-      const uint8_t* block =
-          first < len ? kv_block<D>(a.c, __builtin_amdgcn_readfirstlane(table[page]), h) : nullptr;
+      const uint8_t* block = first < len ? kv_block<D>(a.c, uniform_load(table, page), h) : nullptr;
       if (block) {
         KRegs<D> k;
         k.load(block, lane);
@@ -565,21 +694,35 @@ hipError_t by_shape(int D, int type, int tiles, F f) {
 
 }  // namespace
 
-// Query rows of a head go in the fewest groups of at most max_tiles(D) tiles, of equal size.
+// Query rows of a head go in the fewest groups of at most max_tiles(D) tiles,
+// of equal size.  The grid is what the CUs hold at once, so that no workgroup
+// starts when the others are done; with more than half as many segments it is
+// several times that (and two shares per segment), and the shares' different
+// ends fill each other's gaps.  A share has a page per wavefront at least, two
+// where one tile of queries makes a page cheaper than joining another share;
+// a table of no more pages needs no join.
 AttendPlan kv4_attend_plan(int B, int T, int Hq, int Hk, int D, int width) {
   AttendPlan p;
+  constexpr int kCUs = 256;
   const int tiles = (T * (Hq / Hk) + 15) / 16;
   p.QG = (tiles + max_tiles(D) - 1) / max_tiles(D);
   p.MT = (tiles + p.QG - 1) / p.QG;
+  p.least = p.MT == 1 ? 2 * kWaves : kWaves;
   const int64_t segments = static_cast<int64_t>(B) * Hk * p.QG;
-  int64_t splits = 1024 / segments;
-  const int most = (width + kWaves - 1) / kWaves;
-  splits = splits < 1 ? 1 : (splits > most ? most : splits);
-  p.splits = static_cast<int>(splits);
-  const size_t rows = static_cast<size_t>(segments) * p.splits * p.MT * 16;
-  p.part_off = kSyncBytes;
-  p.stat_off = p.part_off + rows * D * 4;
-  p.total = p.splits > 1 ? p.stat_off + rows * 8 : 0;
+  p.split = width > p.least;
+  int64_t grid = segments;
+  if (p.split) {
+    grid = kCUs * attend_per_cu(D, p.MT);
+    if (2 * segments > grid) grid = 2 * segments > 4 * grid ? 2 * segments : 4 * grid;
+    const int64_t per_segment = static_cast<int64_t>(B) * ((width + p.least - 1) / p.least) * Hk * p.QG;
+    grid = grid < per_segment ? grid : per_segment;
+  }
+  p.grid = grid;
+  const size_t rows = static_cast<size_t>(grid) * p.MT * 16;
+  p.split_off = kSyncBytes;
+  p.stat_off = p.split_off + static_cast<size_t>((segments * sizeof(int2) + 255) / 256 * 256);
+  p.part_off = p.stat_off + rows * 8;
+  p.total = p.split ? p.part_off + rows * D * 4 : 0;
   return p;
 }
 
@@ -587,15 +730,17 @@ hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type,
                                 float* lse, void* workspace, hipStream_t stream) {
   const AttendPlan p = kv4_attend_plan(c.B, T, Hq, c.Hk, c.D, c.width);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  AttendArgs a{c, q, out, lse, nullptr, nullptr, T, Hq, Hq / c.Hk, p.QG, p.splits, scale};
-  if (p.splits > 1) {
+  AttendArgs a{c, q, out, lse, nullptr, nullptr, nullptr, T, Hq, Hq / c.Hk, p.QG, p.least, scale};
+  if (p.split) {
     a.part = reinterpret_cast<float*>(ws + p.part_off);
     a.stat = reinterpret_cast<float*>(ws + p.stat_off);
+    a.split = reinterpret_cast<int2*>(ws + p.split_off);
   }
   const unsigned segments = static_cast<unsigned>(c.B * c.Hk * p.QG);
   return by_shape(c.D, type, p.MT, [&](auto d, auto mt, auto e) {
-    attend<d(), mt(), decltype(e)><<<dim3(segments * p.splits), kThreads, 0, stream>>>(a);
-    if (p.splits > 1) attend_join<d(), mt(), decltype(e)><<<dim3(segments * mt()), kThreads, 0, stream>>>(a);
+    attend<d(), mt(), decltype(e)><<<dim3(static_cast<unsigned>(p.grid)), kThreads, 0, stream>>>(a);
+    if (p.split)
+      attend_join<d(), mt(), decltype(e)><<<dim3(segments * (mt() * 16 * d() / 4 / kThreads)), kThreads, 0, stream>>>(a);
   });
 }
 

@@ -98,7 +98,9 @@ int kv4_attention(const kv4_cache* cache, const kv4_rows* q, int type, int T, in
   if (s) return s;
   if (!out) return SKINNY_EINVAL;
   if (!aligned(out, 16) || !aligned(lse, 4)) return SKINNY_EALIGN;
-  const size_t need = kv4_attend_plan(cache->B, T, Hq, cache->Hk, cache->D, cache->width).total;
+  const AttendPlan plan = kv4_attend_plan(cache->B, T, Hq, cache->Hk, cache->D, cache->width);
+  if (!fits_grid(plan.grid)) return SKINNY_ESHAPE;
+  const size_t need = plan.total;
   if (need) {
     if (!workspace) return SKINNY_EINVAL;
     if (!aligned(workspace, 16)) return SKINNY_EALIGN;
