@@ -76,6 +76,22 @@ __device__ __forceinline__ void kv_codes_store(uint8_t* block, int t, int f, boo
   }
 }
 
+// Half of those: positions 8 piece .. 8 piece + 7.
+template <int D>
+__device__ __forceinline__ uint32_t kv_codes_load_half(const uint8_t* block, int t, int piece, bool v) {
+  const int f = piece / 2, half = piece % 2;
+  if (!v) return *reinterpret_cast<const uint32_t*>(block + KvBlock<D>::k_codes(t, f) + 4 * half);
+  const uint8_t* p = block + KvBlock<D>::v_codes(t, f);
+  if constexpr (D == 256) {
+    return *reinterpret_cast<const uint32_t*>(p + 4 * half);
+  } else if constexpr (D == 128) {
+    return *reinterpret_cast<const uint32_t*>(p + 16 * half);
+  } else {
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p + 32 * half);
+    return static_cast<uint32_t>(q[0]) | (static_cast<uint32_t>(q[8]) << 16);
+  }
+}
+
 template <int D>
 __device__ __forceinline__ int kv_scale_at(int t, int f, bool v) {
   return v ? KvBlock<D>::v_scale(t, f) : KvBlock<D>::k_scale(t, f);
@@ -107,8 +123,41 @@ __device__ __forceinline__ uint8_t* kv_block(const kv4_cache& c, int id, int hea
   return static_cast<uint8_t*>(c.data) + (static_cast<size_t>(id) * c.Hk + head) * KvBlock<D>::kBytes;
 }
 
+// Inclusive sums over the lanes of a wavefront (DPP row shifts and broadcasts).
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);   // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);   // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);   // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31
+  return v;
+}
+
+// The greatest of the lanes' values, in lane 63.
+__device__ __forceinline__ uint32_t wave_greatest(uint32_t v) {
+  const auto with = [&](int o) { v = static_cast<uint32_t>(o) > v ? static_cast<uint32_t>(o) : v; };
+  with(__builtin_amdgcn_update_dpp(v, v, 0x111, 0xf, 0xf, false));
+  with(__builtin_amdgcn_update_dpp(v, v, 0x112, 0xf, 0xf, false));
+  with(__builtin_amdgcn_update_dpp(v, v, 0x114, 0xf, 0xf, false));
+  with(__builtin_amdgcn_update_dpp(v, v, 0x118, 0xf, 0xf, false));
+  with(__builtin_amdgcn_update_dpp(v, v, 0x142, 0xa, 0xf, false));
+  with(__builtin_amdgcn_update_dpp(v, v, 0x143, 0xc, 0xf, false));
+  return v;
+}
+
+__device__ __forceinline__ int lanes_below(unsigned long long mask) {
+  return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
+                                   __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0u));
+}
+
 // 16-bit element types.
 struct F16 {
+  static constexpr uint32_t kInf = 0x7C00u;
+  // v >= 0 rounded towards zero, as bits.
+  static __device__ __forceinline__ uint32_t truncated(float v) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(v, 0.0f)) & 0xFFFFu;
+  }
   static __device__ __forceinline__ float load(uint32_t bits) {
     return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(bits)));
   }
@@ -117,6 +166,8 @@ struct F16 {
   }
 };
 struct BF16 {
+  static constexpr uint32_t kInf = 0x7F80u;
+  static __device__ __forceinline__ uint32_t truncated(float v) { return __float_as_uint(v) >> 16; }
   static __device__ __forceinline__ float load(uint32_t bits) { return __uint_as_float(bits << 16); }
   static __device__ __forceinline__ uint32_t store(float v) {  // to the nearest, ties to even
     return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));

@@ -208,17 +208,6 @@ __device__ __forceinline__ void clean_values(VRegs<D>& v, int first, int len, in
   }
 }
 
-// Inclusive sums over the lanes of a wavefront (DPP row shifts and broadcasts).
-__device__ __forceinline__ int wave_scan(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // row_shr:1
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);   // row_shr:2
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);   // row_shr:4
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);   // row_shr:8
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31
-  return v;
-}
-
 // A workgroup's share of the work: pages p0 .. p1 of one segment (sequence b,
 // head h, query group qg).  The lengths are known to the device only, so every
 // wavefront works the same plan out of them: the least number of pages per

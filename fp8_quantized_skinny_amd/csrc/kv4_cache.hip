@@ -2,6 +2,8 @@
 // reading slots back, and eviction by accumulated weight.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "internal.h"
 #include "kv4.cuh"
 
@@ -12,48 +14,92 @@ constexpr int kThreads = 256;
 
 // 16 values of a head to NVFP4.  The scale is the E4M3 value nearest to
 // amax / (6 g); a code is the E2M1 value nearest to x / (scale * g).  Both
-// are decided on exact numbers: scale * g has at most 28 significant bits, so
-// it and its products with the seven borders between codes are exact in fp64,
-// and each border becomes the least fp32 number on its upper side (values on
-// a border go to the even code).  A code is then a count of integer compares.
+// are decided on exact numbers.
+//
+// The scale: amax has 11 significant bits at most and 6 g 27, so a quotient
+// that is not half way between two E4M3 values is 2^-36 of itself from it at
+// least.  amax * (1 / 6g) in fp64 is off by 2^-52, and rounding it to a
+// multiple of 2^-40 of an E4M3 step first brings those half way back there.
+//
+// A code: scale * g has at most 28 significant bits, so it and its products
+// with the seven borders between codes are exact in fp64, and each border
+// becomes the greatest E value that does not pass it (values on a border go
+// to the even code).  Magnitudes then compare as 16-bit integers, two to a
+// register, and the sign bits of limit - magnitude are the comparisons: c0 ..
+// c6 are a thermometer, so code bit 2 is c3, bit 1 is c1 ^ c3 ^ c5 and bit 0
+// is the parity of all.  Ten operations a value, against 18 for counting fp32
+// comparisons (append of 4 x 8192 tokens, 4 heads of 128: 40 -> 25 us with the
+// page's image below, which is 86 MB at 3.6 TB/s).
 struct Quantized {
   u32x2 codes;
   uint8_t scale;
 };
 
-__device__ __forceinline__ Quantized quantize16(const float (&x)[16], float g) {
-  float amax = 0.0f;
-  bool nan = false;
+typedef short i16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+
+// a where mask is set, b elsewhere; the parity of three.
+__device__ __forceinline__ uint32_t bits_of(uint32_t mask, uint32_t a, uint32_t b) {
+  return __builtin_amdgcn_bitop3_b32(mask, a, b, 0xCA);
+}
+__device__ __forceinline__ uint32_t odd(uint32_t a, uint32_t b, uint32_t c) {
+  return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96);
+}
+
+// Nibbles 0 .. 3 of the low half of v to the even nibbles, of the high half to the odd ones.
+__device__ __forceinline__ uint32_t interleave_nibbles(uint32_t v) {
+  uint32_t lo = v & 0xFFFFu, hi = v >> 16;
+  lo = (lo | (lo << 8)) & 0x00FF00FFu;
+  hi = (hi | (hi << 8)) & 0x00FF00FFu;
+  lo = (lo | (lo << 4)) & 0x0F0F0F0Fu;
+  hi = (hi | (hi << 4)) & 0x0F0F0F0Fu;
+  return lo | (hi << 4);
+}
+
+template <class E>
+__device__ __forceinline__ Quantized quantize16(const u32x4 (&x)[2], double g, double inv6g) {
+  u16x2 most{0, 0};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    amax = fmaxf(amax, fabsf(x[i]));
-    nan |= x[i] != x[i];
-  }
-  double ratio = static_cast<double>(amax) / (6.0 * static_cast<double>(g));
+  for (int i = 0; i < 8; ++i)
+    most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, x[i / 4][i % 4] & 0x7FFF7FFFu));
+  const uint32_t amax = most.x > most.y ? most.x : most.y;
+  const bool nan = amax > E::kInf;
+  double ratio = static_cast<double>(E::load(amax)) * inv6g;
   ratio = ratio < 448.0 ? ratio : 448.0;
   // E4M3: steps of 2^(e-3) in the binade of 2^e, e at least -6.
   int e = ratio >= 0x1p-6 ? static_cast<int>((__double_as_longlong(ratio) >> 52) & 0x7FF) - 1023 : -6;
-  const int steps = static_cast<int>(__builtin_rint(ldexp(ratio, 3 - e)));  // 0 .. 16
+  const int steps = static_cast<int>(__builtin_rint(ldexp(__builtin_rint(ldexp(ratio, 43 - e)), -40)));  // 0 .. 16
   const int byte = (e + 7) * 8 + steps - 8;
-  const double unit = ldexp(static_cast<double>(steps), e - 3) * static_cast<double>(g);
-  uint32_t least[7];
+  const double unit = ldexp(static_cast<double>(steps), e - 3) * g;
+  i16x2 below[7];
   constexpr double kBorder[7] = {0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0};
 #pragma unroll
   for (int i = 0; i < 7; ++i) {
     const double b = kBorder[i] * unit;
-    const float down = __double2float_rz(b);
-    // Even borders (0.25, 1.25, 2.5, 5) belong to the lower code.
-    least[i] = __float_as_uint(down) + ((i % 2 == 0 || static_cast<double>(down) < b) ? 1u : 0u);
+    // Truncating the nearest float gives the greatest E value up to b or the
+    // next one.  Even borders (0.25, 1.25, 2.5, 5) belong to the lower code.
+    const uint32_t down = E::truncated(static_cast<float>(b));
+    const double value = E::load(down);
+    const uint32_t limit = down - ((i % 2 ? value >= b : value > b) ? 1u : 0u);
+    below[i] = __builtin_bit_cast(i16x2, limit | (limit << 16));
   }
-  u32x2 out{0u, 0u};
+  u32x2 out;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t a = __float_as_uint(x[i]) & 0x7FFFFFFFu;
-    uint32_t code = __float_as_uint(x[i]) >> 31 << 3;
+  for (int h = 0; h < 2; ++h) {
+    uint32_t codes = 0u;
 #pragma unroll
-    for (int j = 0; j < 7; ++j) code += a >= least[j];
-    if (i < 8) out.x |= code << (4 * i);
-    else out.y |= code << (4 * (i - 8));
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = x[h][i];
+      const i16x2 a = __builtin_bit_cast(i16x2, w & 0x7FFF7FFFu);
+      uint32_t c[7];
+#pragma unroll
+      for (int j = 0; j < 7; ++j) c[j] = __builtin_bit_cast(uint32_t, below[j] - a);
+      const uint32_t mid = odd(c[1], c[3], c[5]), low = odd(odd(c[0], c[2], c[4]), c[6], mid);
+      constexpr uint32_t kTop = 0x80008000u;
+      const uint32_t code = bits_of(kTop, w, bits_of(kTop, c[3], bits_of(kTop, mid, low >> 1) >> 1) >> 1);
+      codes = bits_of(0xF000F000u, code, codes >> 4);
+    }
+    out[h] = interleave_nibbles(codes);
   }
   Quantized q;
   q.scale = nan ? 0x7F : static_cast<uint8_t>(byte);
@@ -61,8 +107,8 @@ __device__ __forceinline__ Quantized quantize16(const float (&x)[16], float g) {
   return q;
 }
 
-// The places of a workgroup of append and read: sequence, page of the table
-// and head, the pages being those that the newest T slots can reach.
+// The places of a workgroup of append: sequence, page of the table and head,
+// the pages being those that the newest T slots can reach.
 struct Place {
   int b, page, head, len, first;  // first: the oldest slot of the T (may be negative)
 };
@@ -72,116 +118,156 @@ __device__ __forceinline__ bool find_place(const kv4_cache& c, int T, int np, Pl
   p.head = i % c.Hk;
   i /= c.Hk;
   p.b = i / np;
-  p.len = kv_len(c, p.b);
+  p.len = kv_len_uniform(c, p.b);
   p.first = p.len - T;
   p.page = (p.first > 0 ? p.first : 0) / kPage + i % np;
   return p.page * kPage < p.len;
 }
 
+// The page's image in LDS leaves as whole 16-byte vectors.
+template <int D>
+__device__ __forceinline__ void store_image(uint8_t* out, const uint8_t* image) {
+  __syncthreads();
+  for (int i = threadIdx.x; i < KvBlock<D>::kBytes / 16; i += kThreads)
+    reinterpret_cast<u32x4*>(out)[i] = reinterpret_cast<const u32x4*>(image)[i];
+}
+
 // One workgroup per sequence, reached page and head; a thread takes 16 values
-// of a token's key or value.
+// of a token's key or value, and all of its loads are in flight before the
+// first is used.  A page that the step fills is put together in LDS; of one
+// that it shares with older slots only the new tokens' bytes are written.
 template <int D, class E>
-__global__ __launch_bounds__(kThreads) void append(const kv4_cache c, const kv4_rows k, const kv4_rows v, int T, int np) {
+__global__ __launch_bounds__(kThreads) void append(const kv4_cache c, const kv4_rows k, const kv4_rows v, int T, int np,
+                                                   double inv6gk, double inv6gv) {
+  __shared__ __align__(16) uint8_t image[KvBlock<D>::kBytes];
   Place p;
   if (!find_place(c, T, np, p)) return;
-  uint8_t* block = kv_block<D>(c, c.table[static_cast<size_t>(p.b) * c.width + p.page], p.head);
+  uint8_t* block = kv_block<D>(c, uniform_load(c.table, static_cast<int64_t>(p.b) * c.width + p.page), p.head);
   if (!block) return;
-  constexpr int G = KvBlock<D>::kGroups;
-  for (int i = threadIdx.x; i < kPage * G * 2; i += kThreads) {
-    const int f = i % G, t = i / G % kPage;
-    const bool isv = i >= kPage * G;
-    const int slot = p.page * kPage + t, row = slot - p.first;
-    if (row < 0 || slot >= p.len) continue;
-    const kv4_rows& r = isv ? v : k;
-    const u32x4* src = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(r.data) + p.b * r.sequence +
-                                                      row * r.row + p.head * r.head + f * 16);
-    const u32x4 a = src[0], b = src[1];
-    float x[16];
+  constexpr int G = KvBlock<D>::kGroups, kItems = kPage * G * 2 / kThreads, kBatch = kItems < 4 ? kItems : 4;
+  const bool whole = p.page * kPage >= p.first && (p.page + 1) * kPage <= p.len;
+#pragma unroll 1
+  for (int n0 = 0; n0 < kItems; n0 += kBatch) {
+    u32x4 x[kBatch][2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[2 * j] = elem_lo<E>(a[j]);
-      x[2 * j + 1] = elem_hi<E>(a[j]);
-      x[8 + 2 * j] = elem_lo<E>(b[j]);
-      x[8 + 2 * j + 1] = elem_hi<E>(b[j]);
+    for (int n = 0; n < kBatch; ++n) {
+      const int i = (n0 + n) * kThreads + threadIdx.x, f = i % G, t = i / G % kPage;
+      const int slot = p.page * kPage + t, row = slot - p.first;
+      const kv4_rows& r = n0 + n >= kItems / 2 ? v : k;  // kPage * G is a multiple of kThreads
+      if (row >= 0 && slot < p.len) {
+        const u32x4* src = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(r.data) + p.b * r.sequence +
+                                                          row * r.row + p.head * r.head + f * 16);
+        x[n][0] = load16(src);
+        x[n][1] = load16(src + 1);
+      } else {
+        x[n][0] = x[n][1] = u32x4{0u, 0u, 0u, 0u};
+      }
     }
-    const Quantized q = quantize16(x, isv ? c.gv : c.gk);
-    kv_codes_store<D>(block, t, f, isv, q.codes);
-    block[kv_scale_at<D>(t, f, isv)] = q.scale;
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n) {
+      const int i = (n0 + n) * kThreads + threadIdx.x, f = i % G, t = i / G % kPage;
+      const int slot = p.page * kPage + t, row = slot - p.first;
+      if (row < 0 || slot >= p.len) continue;
+      const bool second = n0 + n >= kItems / 2;
+      const Quantized q = quantize16<E>(x[n], second ? c.gv : c.gk, second ? inv6gv : inv6gk);
+      if (whole) {
+        kv_codes_store<D>(image, t, f, second, q.codes);
+        image[kv_scale_at<D>(t, f, second)] = q.scale;
+      } else {
+        kv_codes_store<D>(block, t, f, second, q.codes);
+        block[kv_scale_at<D>(t, f, second)] = q.scale;
+      }
+    }
   }
+  if (whole) store_image<D>(block, image);
 }
 
-// 16 held values from their codes and scale, rounded once to E.
+// Eight held values from their codes and scale, rounded once to E.
 template <class E>
-__device__ __forceinline__ void held16(u32x2 codes, uint32_t scale, float g, u32x4 (&out)[2]) {
+__device__ __forceinline__ u32x4 held8(uint32_t codes, uint32_t scale, float g) {
   const float s = e4m3f<0>(scale);
+  const f16x8 c = e2m1x8(codes);
+  u32x4 out;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const f16x8 c = e2m1x8(codes[h]);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      out[h][j] = elem_pack<E>(static_cast<float>(c[2 * j]) * s * g, static_cast<float>(c[2 * j + 1]) * s * g);
-  }
+  for (int j = 0; j < 4; ++j)
+    out[j] = elem_pack<E>(static_cast<float>(c[2 * j]) * s * g, static_cast<float>(c[2 * j + 1]) * s * g);
+  return out;
 }
 
-// As append, the other way round.  Rows without a slot are zeros: their
-// workgroups are those past the sequence's pages, which there are enough of.
+// One workgroup per sequence, head and 64 rows of the output, whose slots lie
+// in two pages at most; a thread takes eight values, so that neighbours' loads
+// and stores are contiguous.
 template <int D, class E>
 __global__ __launch_bounds__(kThreads) void read_rows(const kv4_cache c, uint16_t* k, uint16_t* v, int n, int np) {
-  constexpr int G = KvBlock<D>::kGroups;
+  constexpr int P = D / 8, kItems = kPage * P * 2 / kThreads, kBatch = kItems < 8 ? kItems : 8;
   const int h = blockIdx.x % c.Hk;
   const int64_t at = blockIdx.x / c.Hk;
   const int b = static_cast<int>(at / np);
-  const int row0 = static_cast<int>(at % np) * kPage;  // 64 rows of the output
-  const int len = kv_len(c, b);
-  for (int i = threadIdx.x; i < kPage * G * 2; i += kThreads) {
-    const int f = i % G, row = row0 + i / G % kPage;
-    const bool isv = i >= kPage * G;
-    if (row >= n) continue;
-    const int slot = len - n + row;
-    u32x4 out[2] = {u32x4{0u, 0u, 0u, 0u}, u32x4{0u, 0u, 0u, 0u}};
-    if (slot >= 0) {
-      const uint8_t* block = kv_block<D>(c, c.table[static_cast<size_t>(b) * c.width + slot / kPage], h);
-      if (block) {
+  const int row0 = static_cast<int>(at % np) * kPage;
+  const int first = kv_len_uniform(c, b) - n + row0;  // slot of the first row
+  const uint8_t* block[2] = {nullptr, nullptr};
+  const int p0 = (first > 0 ? first : 0) / kPage;
+  const int slots = first + (n - row0 < kPage ? n - row0 : kPage);  // past the last row's slot
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if ((p0 + i) * kPage < slots)
+      block[i] = kv_block<D>(c, uniform_load(c.table, static_cast<int64_t>(b) * c.width + p0 + i), h);
+#pragma unroll 1
+  for (int n0 = 0; n0 < kItems; n0 += kBatch) {
+    uint32_t codes[kBatch], scale[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = (n0 + u) * kThreads + threadIdx.x, piece = i % P, r = i / P % kPage;
+      const bool isv = n0 + u >= kItems / 2;
+      const int slot = first + r;
+      const uint8_t* from = slot / kPage == p0 ? block[0] : block[1];
+      codes[u] = scale[u] = 0u;
+      if (slot >= 0 && row0 + r < n && from) {
         const int t = slot % kPage;
-        held16<E>(kv_codes_load<D>(block, t, f, isv), block[kv_scale_at<D>(t, f, isv)], isv ? c.gv : c.gk, out);
+        codes[u] = kv_codes_load_half<D>(from, t, piece, isv);
+        scale[u] = from[kv_scale_at<D>(t, piece / 2, isv)];
       }
     }
-    u32x4* dst = reinterpret_cast<u32x4*>((isv ? v : k) + ((static_cast<size_t>(b) * n + row) * c.Hk + h) * D + f * 16);
-    dst[0] = out[0];
-    dst[1] = out[1];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = (n0 + u) * kThreads + threadIdx.x, piece = i % P, r = i / P % kPage;
+      const bool isv = n0 + u >= kItems / 2;
+      if (row0 + r >= n) continue;
+      uint16_t* dst = (isv ? v : k) + ((static_cast<size_t>(b) * n + row0 + r) * c.Hk + h) * D + piece * 8;
+      *reinterpret_cast<u32x4*>(dst) = held8<E>(codes[u], scale[u], isv ? c.gv : c.gk);
+    }
   }
 }
 
 // ---- eviction ---------------------------------------------------------------
 constexpr int kSelectThreads = 1024;
+constexpr int kSelectWaves = kSelectThreads / 64;
+constexpr int kRows = 8;                             // most groups of four keys of a thread in LDS
+constexpr int kRowSlots = 4 * kSelectThreads;
+constexpr int kTileSlots = kRows * kRowSlots;
 constexpr int kBins = 2048;
+constexpr uint32_t kOutside = 0u, kSure = 0xFFFFFFFFu;
 
-// Orders like the weight; a NaN is the least.
+// Orders like the weight, between kOutside and kSure; a NaN is the least.
 __device__ __forceinline__ uint32_t weight_key(float w) {
-  if (w != w) return 0u;
+  if (w != w) return 1u;
   const uint32_t b = __float_as_uint(w + 0.0f);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
 // Exclusive sums over the workgroup's threads; every thread also gets the total.
-__device__ __forceinline__ int block_scan(int v, int* tmp, int& total) {
+__device__ __forceinline__ int2 block_scan(int2 v, int2* tmp, int2& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int s = v;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(s, o);
-    if (lane >= o) s += u;
-  }
+  const int2 s{wave_scan(v.x), wave_scan(v.y)};
   __syncthreads();
   if (lane == 63) tmp[wave] = s;
   __syncthreads();
-  int before = 0;
-  total = 0;
-  for (int w = 0; w < kSelectThreads / 64; ++w) {
-    if (w < wave) before += tmp[w];
-    total += tmp[w];
-  }
-  return before + s - v;
+  int2 part = lane < kSelectWaves ? tmp[lane] : int2{0, 0};
+  part = int2{wave_scan(part.x), wave_scan(part.y)};
+  const int w = __builtin_amdgcn_readfirstlane(wave);
+  total = int2{__builtin_amdgcn_readlane(part.x, 63), __builtin_amdgcn_readlane(part.y, 63)};
+  const int2 before{w ? __builtin_amdgcn_readlane(part.x, w - 1) : 0, w ? __builtin_amdgcn_readlane(part.y, w - 1) : 0};
+  return int2{before.x + s.x - v.x, before.y + s.y - v.y};
 }
 
 // One workgroup per sequence and head finds the key of the last slot kept by
@@ -189,63 +275,118 @@ __device__ __forceinline__ int block_scan(int v, int* tmp, int& total) {
 // bin that holds the wanted rank, and again within it until it is one key (at
 // most three times for 32-bit keys).  Equal-width bins between the least and
 // the greatest key spread weights that differ by factors over many bins.
+//
+// The keys lie in LDS, where a thread finds those that it put there itself,
+// four neighbours together: up to 32768 slots are read once, and longer
+// sequences again, 32768 at a time, in each of the passes.  The loops stay
+// short: with the keys in registers instead, the unrolled passes are 50 KB of
+// code that runs once, and fetching it took longer than the work.  16
+// sequences x 4 heads of 20000 .. 32768 slots, keeping 8192: 29 us (91 with a
+// run of slots per thread, read four times over); one of 4133: 13 us (21).
 __global__ __launch_bounds__(kSelectThreads) void select_slots(const kv4_cache c, const float* acc, int dst_width,
                                                                int32_t* kept, int32_t* new_lens, float* new_acc,
                                                                int keep, int sinks, int recent) {
   __shared__ int bins[kBins];
-  __shared__ int tmp[kSelectThreads / 64];
+  __shared__ int2 tmp[kSelectWaves];
   __shared__ uint32_t range[2];
   __shared__ int found[2];
-  const int tid = threadIdx.x;
+  __shared__ int2 count[kRows * kSelectWaves];  // of a wavefront's 256 slots: those above the last key, those equal to it
+  const unsigned tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;  // slots of a tile may pass 2^31
   const int h = blockIdx.x % c.Hk, b = blockIdx.x / c.Hk;
-  const int n = kv_len(c, b);
+  const unsigned n = kv_len_uniform(c, b);
   const float* w = acc + (static_cast<size_t>(b) * c.Hk + h) * c.width * kPage;
   int32_t* ids = kept + (static_cast<size_t>(b) * c.Hk + h) * keep;
   float* out = new_acc + (static_cast<size_t>(b) * c.Hk + h) * dst_width * kPage;
-  const int m = n < keep ? n : keep;
+  const unsigned most = keep, places = dst_width * kPage, m = n < most ? n : most;
   if (h == 0 && tid == 0) new_lens[b] = m;
-  for (int i = m + tid; i < keep; i += kSelectThreads) ids[i] = -1;
-  for (int i = m + tid; i < dst_width * kPage; i += kSelectThreads) out[i] = 0.0f;
-  if (n <= keep) {
-    for (int i = tid; i < n; i += kSelectThreads) {
+  for (unsigned i = m + tid; i < most; i += kSelectThreads) ids[i] = -1;
+  for (unsigned i = m + tid; i < places; i += kSelectThreads) out[i] = 0.0f;
+  if (n <= most) {
+    for (unsigned i = tid; i < n; i += kSelectThreads) {
       ids[i] = i;
       out[i] = w[i];
     }
     return;
   }
   // More slots than stay: those between the sinks and the recent ones compete.
-  const int lo_slot = sinks, hi_slot = n - recent;
+  const unsigned lo_slot = sinks, hi_slot = n - recent;
   int need = keep - sinks - recent;
-  uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-  for (int i = lo_slot + tid; i < hi_slot; i += kSelectThreads) {
-    const uint32_t key = weight_key(w[i]);
-    lo = key < lo ? key : lo;
-    hi = key > hi ? key : hi;
-  }
+  extern __shared__ u32x4 keys[];  // [kRows or fewer][kSelectThreads]
+  const auto rows = [&](unsigned base) {
+    const unsigned left = n - base;
+    return left < kTileSlots ? (left + kRowSlots - 1) / kRowSlots : static_cast<unsigned>(kRows);
+  };
+  const auto load = [&](unsigned base) __attribute__((always_inline)) {
+    const unsigned all = rows(base);
+#pragma unroll 1
+    for (unsigned i0 = 0; i0 < all; i0 += 4) {
+      u32x4 held[4];
+#pragma unroll
+      for (unsigned i = 0; i < 4; ++i) {
+        const unsigned s = base + (i0 + i) * kRowSlots + tid * 4;  // acc has whole pages: s + 3 is within it
+        held[i] = *reinterpret_cast<const u32x4*>(w + (s < n ? s : 0u));
+      }
+#pragma unroll
+      for (unsigned i = 0; i < 4; ++i) {
+        u32x4 k;
+#pragma unroll
+        for (unsigned e = 0; e < 4; ++e) {
+          const unsigned s = base + (i0 + i) * kRowSlots + tid * 4 + e;
+          k[e] = s >= n ? kOutside : (s < lo_slot || s >= hi_slot ? kSure : weight_key(__uint_as_float(held[i][e])));
+        }
+        if (i0 + i < all) keys[(i0 + i) * kSelectThreads + tid] = k;
+      }
+    }
+  };
+  // f over the thread's keys of every tile.
+  const auto each = [&](auto f) __attribute__((always_inline)) {
+    for (unsigned base = 0;; base += kTileSlots) {
+      if (n > kTileSlots) load(base);
+      const unsigned all = rows(base);
+#pragma unroll 4
+      for (unsigned i = 0; i < all; ++i) {
+        const u32x4 k = keys[i * kSelectThreads + tid];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f(k[e]);
+      }
+      if (n - base <= kTileSlots) break;
+    }
+  };
+  if (n <= kTileSlots) load(0);
   if (tid == 0) {
-    range[0] = 0xFFFFFFFFu;
+    range[0] = kSure;
     range[1] = 0u;
   }
   __syncthreads();
-  atomicMin(&range[0], lo);
-  atomicMax(&range[1], hi);
+  uint32_t lo = kSure, hi = 0u;
+  each([&](uint32_t k) __attribute__((always_inline)) {
+    if (k != kOutside && k != kSure) {
+      lo = k < lo ? k : lo;
+      hi = k > hi ? k : hi;
+    }
+  });
+  lo = ~wave_greatest(~lo);
+  hi = wave_greatest(hi);
+  if (lane == 63) {
+    atomicMin(&range[0], lo);
+    atomicMax(&range[1], hi);
+  }
   __syncthreads();
   lo = range[0];
   hi = range[1];
   while (need > 0 && lo < hi) {
     int shift = 0;
     while (((hi - lo) >> shift) >= kBins) ++shift;
-    for (int i = tid; i < kBins; i += kSelectThreads) bins[i] = 0;
+    for (unsigned i = tid; i < kBins; i += kSelectThreads) bins[i] = 0;
     __syncthreads();
-    for (int i = lo_slot + tid; i < hi_slot; i += kSelectThreads) {
-      const uint32_t key = weight_key(w[i]);
-      if (key >= lo && key <= hi) atomicAdd(&bins[(key - lo) >> shift], 1);
-    }
+    each([&](uint32_t k) __attribute__((always_inline)) {
+      if (k - lo <= hi - lo) atomicAdd(&bins[(k - lo) >> shift], 1);
+    });
     __syncthreads();
     // Bins from the top: thread t has bins kBins-1-2t and kBins-2-2t.
-    const int top = kBins - 1 - 2 * tid, a = bins[top], d = bins[top - 1];
-    int total;
-    const int above = block_scan(a + d, tmp, total);
+    const int top = kBins - 1 - 2 * static_cast<int>(tid), a = bins[top], d = bins[top - 1];
+    int2 total;
+    const int above = block_scan(int2{a + d, 0}, tmp, total).x;
     if (above < need && need <= above + a + d) {
       const bool first = need <= above + a;
       found[0] = first ? top : top - 1;
@@ -260,68 +401,122 @@ __global__ __launch_bounds__(kSelectThreads) void select_slots(const kv4_cache c
     __syncthreads();
     if (shift == 0) hi = lo;
   }
-  // Every key above lo stays, and `need` of those equal to it, the lowest slots.
-  const uint32_t edge = need > 0 ? lo : 0xFFFFFFFFu;
-  const int per = (n + kSelectThreads - 1) / kSelectThreads;
-  const int s0 = tid * per, s1 = s0 + per < n ? s0 + per : n;
-  int above = 0, equal = 0;
-  for (int s = s0; s < s1; ++s) {
-    const uint32_t key = s < sinks || s >= hi_slot ? 0xFFFFFFFFu : weight_key(w[s]);
-    above += s < sinks || s >= hi_slot || (key > edge);
-    equal += key == edge && s >= sinks && s < hi_slot;
-  }
-  int total;
-  int left = need - block_scan(equal, tmp, total);
-  left = left < 0 ? 0 : left;
-  int at = block_scan(above + (equal < left ? equal : left), tmp, total);
-  for (int s = s0; s < s1; ++s) {
-    const float weight = w[s];
-    const bool sure = s < sinks || s >= hi_slot;
-    const uint32_t key = weight_key(weight);
-    const bool tie = !sure && key == edge && left > 0;
-    if (tie) --left;
-    if (sure || key > edge || tie) {
-      ids[at] = s;
-      out[at] = weight;
-      ++at;
+  // Every key above lo stays, and `need` of those equal to it, the lowest
+  // slots: a slot's place is the number of slots before it that stay.
+  const uint32_t edge = need > 0 ? lo : kSure - 1u;
+  int2 before{0, 0};
+  for (unsigned base = 0;; base += kTileSlots) {
+    if (n > kTileSlots) load(base);
+    const unsigned all = rows(base);
+#pragma unroll 4
+    for (unsigned i = 0; i < all; ++i) {
+      const u32x4 k = keys[i * kSelectThreads + tid];
+      int above = 0, equal = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        above += __popcll(__ballot(k[e] > edge));
+        equal += __popcll(__ballot(k[e] == edge));
+      }
+      if (lane == 0) count[i * kSelectWaves + wave] = int2{above, equal};
     }
+    __syncthreads();
+    int2 total;
+    const int2 mine = block_scan(tid < all * kSelectWaves ? count[tid] : int2{0, 0}, tmp, total);
+    if (tid < all * kSelectWaves) count[tid] = int2{before.x + mine.x, before.y + mine.y};
+    __syncthreads();
+#pragma unroll 4
+    for (unsigned i = 0; i < all; ++i) {
+      const u32x4 k = keys[i * kSelectThreads + tid];
+      int above = count[i * kSelectWaves + wave].x, equal = count[i * kSelectWaves + wave].y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        above += lanes_below(__ballot(k[e] > edge));
+        equal += lanes_below(__ballot(k[e] == edge));
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (k[e] > edge || (k[e] == edge && equal < need)) {
+          const int place = above + (equal < need ? equal : need);
+          const unsigned s = base + i * kRowSlots + tid * 4 + e;
+          ids[place] = s;
+          out[place] = w[s];
+        }
+        above += k[e] > edge;
+        equal += k[e] == edge;
+      }
+    }
+    before.x += total.x;
+    before.y += total.y;
+    if (n - base <= kTileSlots) break;
+    __syncthreads();
   }
 }
 
 // One workgroup per page written: its tokens' codes and scales are gathered
-// into LDS and leave as one block.
+// into LDS, all loads in flight at once, and leave as one block.  Neighbours
+// among the kept slots share lines of the source, so each load's lanes are
+// chosen to meet in them: 64 tokens for one piece of K, and of the scales, and
+// four tokens for the whole of V, whose 16 pieces lie in two lines.  Bound by
+// memory: keeping a third of the slots touches nearly every line of the
+// source, so 16 sequences x 4 heads x 8192 slots kept of 20000 .. 32768 read
+// 232 MB and write 75 MB, in 94 us.
 template <int D>
 __global__ __launch_bounds__(kThreads) void copy_kept(const kv4_cache c, const kv4_cache dst, const int32_t* kept,
                                                       int keep, int np) {
-  __shared__ __align__(16) uint8_t image[KvBlock<D>::kBytes];
-  constexpr int G = KvBlock<D>::kGroups;
+  using Block = KvBlock<D>;
+  using KPiece = std::conditional_t<D == 64, u32x2, u32x4>;
+  using KScales = std::conditional_t<D == 64, uint8_t, std::conditional_t<D == 128, uint16_t, uint32_t>>;
+  using VPiece = std::conditional_t<D == 64, uint16_t, std::conditional_t<D == 128, uint32_t, u32x2>>;
+  constexpr int kKPieces = D == 256 ? 2 : 1, kVScales = D / 64, kVPieces = kPage * 16 / kThreads;
+  __shared__ __align__(16) uint8_t image[Block::kBytes];
+  __shared__ const uint8_t* from[kPage];  // each token's block
+  __shared__ int token[kPage];
   const int h = blockIdx.x % c.Hk;
   const int64_t at = blockIdx.x / c.Hk;
   const int b = static_cast<int>(at / np), page = static_cast<int>(at % np);
-  const int n = kv_len(c, b), m = n < keep ? n : keep;
+  const int n = kv_len_uniform(c, b), m = n < keep ? n : keep;
   if (page * kPage >= m) return;
-  uint8_t* out = kv_block<D>(dst, dst.table[static_cast<size_t>(b) * dst.width + page], h);
+  uint8_t* out = kv_block<D>(dst, uniform_load(dst.table, static_cast<int64_t>(b) * dst.width + page), h);
   if (!out) return;
-  const int32_t* ids = kept + (static_cast<size_t>(b) * c.Hk + h) * keep + page * kPage;
-  for (int i = threadIdx.x; i < kPage * G * 2; i += kThreads) {
-    const int f = i % G, t = i / G % kPage;
-    const bool isv = i >= kPage * G;
-    u32x2 codes{0u, 0u};
-    uint8_t scale = 0;
-    if (page * kPage + t < m) {
-      const int slot = ids[t];
-      const uint8_t* block = kv_block<D>(c, c.table[static_cast<size_t>(b) * c.width + slot / kPage], h);
-      if (block) {
-        codes = kv_codes_load<D>(block, slot % kPage, f, isv);
-        scale = block[kv_scale_at<D>(slot % kPage, f, isv)];
-      }
-    }
-    kv_codes_store<D>(image, t, f, isv, codes);
-    image[kv_scale_at<D>(t, f, isv)] = scale;
+  if (threadIdx.x < kPage) {
+    const int place = page * kPage + threadIdx.x;
+    const int slot = place < m ? kept[(static_cast<size_t>(b) * c.Hk + h) * keep + place] : -1;
+    from[threadIdx.x] = slot < 0 ? nullptr : kv_block<D>(c, c.table[static_cast<size_t>(b) * c.width + slot / kPage], h);
+    token[threadIdx.x] = slot % kPage;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < KvBlock<D>::kBytes / 16; i += kThreads)
-    reinterpret_cast<u32x4*>(out)[i] = reinterpret_cast<const u32x4*>(image)[i];
+  const int lane = threadIdx.x & 63, quarter = threadIdx.x >> 6, column = threadIdx.x % 16;
+  const uint8_t* block = from[lane];
+  const int t = token[lane];
+  KPiece kc[kKPieces]{};
+  KScales ks{};
+  uint8_t vs[kVScales]{};
+  VPiece vc[kVPieces]{};
+  if (block) {
+#pragma unroll
+    for (int i = 0; i < kKPieces; ++i)
+      kc[i] = *reinterpret_cast<const KPiece*>(block + Block::k_codes(t, quarter * (D / 64) + 2 * i));
+    ks = *reinterpret_cast<const KScales*>(block + Block::k_scale(t, quarter * (D / 64)));
+#pragma unroll
+    for (int i = 0; i < kVScales; ++i) vs[i] = block[Block::v_scale(t, quarter * kVScales + i)];
+  }
+#pragma unroll
+  for (int i = 0; i < kVPieces; ++i) {
+    const int j = i * (kThreads / 16) + threadIdx.x / 16;
+    if (from[j]) vc[i] = *reinterpret_cast<const VPiece*>(from[j] + Block::v_codes(token[j], 0) + column * 16);
+  }
+#pragma unroll
+  for (int i = 0; i < kKPieces; ++i)
+    *reinterpret_cast<KPiece*>(image + Block::k_codes(lane, quarter * (D / 64) + 2 * i)) = kc[i];
+  *reinterpret_cast<KScales*>(image + Block::k_scale(lane, quarter * (D / 64))) = ks;
+#pragma unroll
+  for (int i = 0; i < kVScales; ++i) image[Block::v_scale(lane, quarter * kVScales + i)] = vs[i];
+#pragma unroll
+  for (int i = 0; i < kVPieces; ++i) {
+    const int j = i * (kThreads / 16) + threadIdx.x / 16;
+    *reinterpret_cast<VPiece*>(image + Block::v_codes(j, 0) + column * 16) = vc[i];
+  }
+  store_image<D>(out, image);
 }
 
 template <class F>
@@ -340,9 +535,10 @@ hipError_t launch_kv4_append(const kv4_cache& c, const kv4_rows& k, const kv4_ro
                              hipStream_t stream) {
   const int np = pages_of_rows(T);
   const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(c.B) * np * c.Hk));
+  const double ik = 1.0 / (6.0 * static_cast<double>(c.gk)), iv = 1.0 / (6.0 * static_cast<double>(c.gv));
   return by_head_size(c.D, [&](auto d) {
-    if (type == SKINNY_F16) append<d(), F16><<<grid, kThreads, 0, stream>>>(c, k, v, T, np);
-    else append<d(), BF16><<<grid, kThreads, 0, stream>>>(c, k, v, T, np);
+    if (type == SKINNY_F16) append<d(), F16><<<grid, kThreads, 0, stream>>>(c, k, v, T, np, ik, iv);
+    else append<d(), BF16><<<grid, kThreads, 0, stream>>>(c, k, v, T, np, ik, iv);
   });
 }
 
@@ -357,7 +553,9 @@ hipError_t launch_kv4_read(const kv4_cache& c, uint16_t* k, uint16_t* v, int typ
 
 hipError_t launch_kv4_evict(const kv4_cache& c, const float* acc, const kv4_cache& dst, int32_t* kept,
                             int32_t* new_lens, float* new_acc, int keep, int sinks, int recent, hipStream_t stream) {
-  select_slots<<<dim3(static_cast<unsigned>(c.B * c.Hk)), kSelectThreads, 0, stream>>>(
+  const int64_t held = (static_cast<int64_t>(c.width) * kPage + kRowSlots - 1) / kRowSlots;
+  const size_t lds = static_cast<size_t>(held < kRows ? held : kRows) * kRowSlots * sizeof(uint32_t);
+  select_slots<<<dim3(static_cast<unsigned>(c.B * c.Hk)), kSelectThreads, lds, stream>>>(
       c, acc, dst.width, kept, new_lens, new_acc, keep, sinks, recent);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

@@ -112,11 +112,6 @@ __device__ __forceinline__ Key kth_key(const Key (&key)[N], int k) {
   return at;
 }
 
-__device__ __forceinline__ int lanes_below(unsigned long long mask) {
-  return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
-                                   __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0u));
-}
-
 // A wavefront's list of keys.
 struct List {
   Key* keys;    // LDS, kList of them
