@@ -5,13 +5,14 @@
 //
 // Every lane keeps the statistics of the elements it met about its own running
 // maximum.  The alternatives: a logit and its index form one 64-bit key that
-// orders as wanted (argmax_key), all keys of a row differ, and keys at or
-// below a threshold under which k greater ones are known need no further look.
-// A wavefront collects the keys above the threshold in a list of its own in
-// LDS, cuts the list back to its k greatest when it has grown long, and raises
-// the threshold, which the workgroup's wavefronts share, to the least of
-// those.  After the first elements few get past it: the pass costs one
-// comparison of a lane's maximum per 16 elements.
+// orders as wanted (argmax_key), and all keys of a row differ.  The elements of
+// a 16-byte load are a group with the key of its greatest logit and its first
+// index.  The k greatest elements lie in the k greatest groups, so a wavefront
+// collects group keys only: those above a threshold that k groups are known to
+// reach go to a list of its own in LDS, which is cut back when it has grown
+// long, and the threshold, which the workgroup's wavefronts share, rises.  The
+// pass pays one comparison per load for it (and a few operations where a lane
+// has something to add); the groups that are left at the end are read again.
 #include <hip/hip_runtime.h>
 
 #include "internal.h"
@@ -27,8 +28,10 @@ constexpr int kThreads = 64 * kWaves;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kVectors = 2;                      // 16-byte loads of a lane per step
 constexpr int kMost = kVectors * 8;              // elements of a lane per step
+constexpr int kCut = 64;                         // most keys that a cut leaves
 constexpr int kKeep = 128;                       // keys at which a list is cut back
-constexpr int kList = SKINNY_MAX_TOP * kMost + kKeep;  // see collect()
+constexpr int kList = kKeep + 64 * kVectors;     // a step adds kVectors keys per lane at most
+static_assert(SKINNY_MAX_TOP <= kCut, "a cut leaves k keys at least");
 
 struct F32 {
   using T = float;
@@ -87,10 +90,15 @@ __device__ __forceinline__ Stat join(const Stat& a, const Stat& b) {
   return Stat{m, x.s + y.s, x.t + y.t};
 }
 
-__device__ __forceinline__ uint32_t key_high(float v) { return static_cast<uint32_t>(argmax_key(v, 0) >> 32); }
+// The logit of a key (-0 became 0).
+__device__ __forceinline__ float key_value(Key key) {
+  const uint32_t ord = static_cast<uint32_t>(key >> 32);
+  return __uint_as_float((ord & 0x80000000u) ? ord ^ 0x80000000u : ~ord);
+}
+__device__ __forceinline__ int key_index(Key key) { return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(key)); }
 
-// The k-th greatest of the wavefront's keys (N per lane), by bits from the
-// top; 0 if there are fewer than k keys other than 0.
+// A value that k .. kCut of the wavefront's keys (N per lane, all different or
+// 0) reach, by bits from the top; 0 if fewer than k keys are not 0.
 template <int N>
 __device__ __forceinline__ Key kth_key(const Key (&key)[N], int k) {
   Key at = 0ull;
@@ -101,12 +109,7 @@ __device__ __forceinline__ Key kth_key(const Key (&key)[N], int k) {
     for (int i = 0; i < N; ++i) n += __popcll(__ballot(key[i] >= next));
     if (n >= k) {
       at = next;
-      if (n == k) {  // the least of exactly k keys
-        Key least = ~0ull;
-#pragma unroll
-        for (int i = 0; i < N; ++i) least = key[i] >= next && key[i] < least ? key[i] : least;
-        return ~wave_max_key(~least);
-      }
+      if (n <= kCut) break;
     }
   }
   return at;
@@ -118,12 +121,13 @@ struct List {
   int n;
   int k;
   Key over;     // keys at or below it are not wanted
+  float floor;  // logits below it are not
   Key* shared;  // LDS: the greatest `over` of the workgroup's wavefronts
 
   __device__ __forceinline__ void raise(Key to) {
     if (to > over) {
       over = to;
-      if ((threadIdx.x & 63) == 0) atomicMax(shared, to);
+      floor = key_value(to);
     }
   }
   __device__ __forceinline__ void push(bool want, Key key) {
@@ -131,17 +135,12 @@ struct List {
     if (want) keys[n + lanes_below(mask)] = key;
     n += __popcll(mask);
   }
-  // Cuts the list back to its k greatest keys (fewer if it has no more).
-  __device__ void cut() {
-    if (n <= k) return;
-    constexpr int kPer = (kList + 63) / 64;
+  // Cuts the list back to at most kCut keys, the k greatest among them.
+  __device__ __forceinline__ void cut() {
+    if (n <= kCut) return;
+    constexpr int N = kList / 64;
     const int lane = threadIdx.x & 63;
     __builtin_amdgcn_wave_barrier();
-    if (n <= 192) cut_held<3>(lane);
-    else cut_held<kPer>(lane);
-  }
-  template <int N>
-  __device__ __forceinline__ void cut_held(int lane) {
     Key held[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) held[i] = i * 64 + lane < n ? keys[i * 64 + lane] : 0ull;
@@ -149,38 +148,23 @@ struct List {
     n = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) push(held[i] >= least && held[i] > 0ull, held[i]);
-    raise(least);
+    if (least - 1ull > over && least > 0ull) {
+      raise(least - 1ull);
+      if (lane == 0) atomicMax(shared, over);
+    }
   }
 };
 
-// One step of a wavefront: N elements per lane, element i of a lane at column
-// at(i), real where real(i).  `top` is the greatest of a lane's elements.
-template <int N, class At, class Real>
-__device__ __forceinline__ void collect(List& list, const float (&x)[N], float top, At at, Real real) {
-  const Key shared = *static_cast<volatile Key*>(list.shared);
-  if (shared > list.over) list.over = shared;
-  const unsigned long long lanes = __ballot(key_high(top) >= static_cast<uint32_t>(list.over >> 32));
-  if (lanes == 0ull) return;
-  if (list.n + __popcll(lanes) * N > kList) {
-    // Room for every lane's elements is not sure: let the lanes' greatest keys
-    // decide.  k of them reach the k-th greatest, so nothing below it is
-    // wanted, and only the k lanes that reach it hold anything above it: at
-    // most k N keys, which the list has room for after a cut.
-    list.cut();
-    Key best[1] = {0ull};
+// The groups of one step of a wavefront: U per lane, with their greatest logits
+// and first columns; `top` is the greatest of a lane's logits.
+template <int U, class At, class Real>
+__device__ __forceinline__ void collect(List& list, const float (&most)[U], float top, At at, Real real) {
+  if (!__any(top >= list.floor)) return;
+  list.raise(*static_cast<volatile Key*>(list.shared));
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const Key key = real(i) ? argmax_key(x[i], at(i)) : 0ull;
-      best[0] = key > best[0] ? key : best[0];
-    }
-    const Key kth = kth_key<1>(best, list.k);
-    if (kth > 0ull) list.raise(kth - 1ull);
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const Key key = argmax_key(x[i], at(i));
-    const bool want = real(i) && key > list.over;
-    if (__any(want)) list.push(want, key);
+  for (int u = 0; u < U; ++u) {
+    const Key key = argmax_key(most[u], at(u));  // 0 if all are NaN
+    list.push(real(u) && key > list.over, key);
   }
   if (list.n > kKeep) list.cut();
 }
@@ -197,14 +181,75 @@ __device__ __forceinline__ void add(Stat& st, const float (&x)[N], float top) {
   }
 }
 
+// Sums and the greatest over the lanes of a wavefront, in lane 63.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float old, float v) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(__float_as_uint(old), __float_as_uint(v), CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ float lanes_sum(float v) {
+  v += dpp<0x111, 0xf>(0.0f, v);
+  v += dpp<0x112, 0xf>(0.0f, v);
+  v += dpp<0x114, 0xf>(0.0f, v);
+  v += dpp<0x118, 0xf>(0.0f, v);
+  v += dpp<0x142, 0xa>(0.0f, v);
+  v += dpp<0x143, 0xc>(0.0f, v);
+  return v;
+}
+__device__ __forceinline__ float lanes_greatest(float v) {
+  v = fmaxf(v, dpp<0x111, 0xf>(v, v));
+  v = fmaxf(v, dpp<0x112, 0xf>(v, v));
+  v = fmaxf(v, dpp<0x114, 0xf>(v, v));
+  v = fmaxf(v, dpp<0x118, 0xf>(v, v));
+  v = fmaxf(v, dpp<0x142, 0xa>(v, v));
+  v = fmaxf(v, dpp<0x143, 0xc>(v, v));
+  return v;
+}
+__device__ __forceinline__ float lane_63(float v) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
+}
 __device__ __forceinline__ Stat wave_join(Stat st) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) st = join(st, Stat{__shfl_xor(st.m, o), __shfl_xor(st.s, o), __shfl_xor(st.t, o)});
-  return st;
+  const float m = lane_63(lanes_greatest(st.m));
+  st = moved(st, m);
+  return Stat{m, lane_63(lanes_sum(st.s)), lane_63(lanes_sum(st.t))};
 }
 
-// Results of row r from its statistics and its n candidate keys in LDS (k
-// greatest among them, zeros allowed).
+// The workgroup's lists in one: at most kCut keys, the k greatest of all among
+// them, in `out`; returns their number.  A barrier comes first and last.
+__device__ __forceinline__ int merge_lists(const Key (*lists)[kList], const int* counts, int k, Key* out, int* number) {
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    constexpr int kPer = kKeep / 64, N = kWaves * kPer;
+    Key held[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int j = i % kPer * 64 + lane;
+      held[i] = j < counts[i / kPer] ? lists[i / kPer][j] : 0ull;
+    }
+    const Key least = kth_key<N>(held, k);
+    List all{out, 0, k, 0ull, 0.0f, nullptr};
+#pragma unroll
+    for (int i = 0; i < N; ++i) all.push(held[i] >= least && held[i] > 0ull, held[i]);
+    if (lane == 0) *number = all.n;
+  }
+  __syncthreads();
+  return *number;
+}
+
+// rank(i) < k of the n different keys in LDS goes to put(rank, key), and so do
+// the places for which there is no key, as 0.
+template <class Put>
+__device__ __forceinline__ void ranked(const Key* keys, int n, int k, Put put) {
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const Key key = keys[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += keys[j] > key;
+    if (rank < k) put(rank, key);
+  }
+  for (int i = n + threadIdx.x; i < k; i += kThreads) put(i, 0ull);
+}
+
+// Results of row r from its statistics and its n candidate keys in LDS.
 template <class L>
 __device__ __forceinline__ void finish(const LogprobArgs& a, int r, const typename L::T* x, const Stat& st,
                                        const Key* keys, int n) {
@@ -216,17 +261,11 @@ __device__ __forceinline__ void finish(const LogprobArgs& a, int r, const typena
     a.logprob[r] = token >= 0 && token < a.V ? L::at(x + token) - m - log : NAN;
     a.entropy[r] = none ? 0.0f : log - st.t / st.s;
   }
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const Key key = keys[i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += keys[j] > key || (keys[j] == key && j < i);
-    if (rank < a.k) {
-      const int id = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(key));  // -1 for no key
-      const size_t at = static_cast<size_t>(r) * a.k + rank;
-      a.top_ids[at] = id;
-      a.top_logprobs[at] = id < 0 ? NAN : L::at(x + id) - m - log;
-    }
-  }
+  ranked(keys, n, a.k, [&](int rank, Key key) {
+    const size_t at = static_cast<size_t>(r) * a.k + rank;
+    a.top_ids[at] = key ? key_index(key) : -1;
+    a.top_logprobs[at] = key ? key_value(key) - m - log : NAN;
+  });
 }
 
 __device__ __forceinline__ void put(Key* p, Key v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
@@ -242,14 +281,20 @@ __global__ __launch_bounds__(kThreads) void logprobs(const LogprobArgs a) {
   using T = typename L::T;
   constexpr int kPer = L::kPer, N = kVectors * kPer;
   __shared__ Key lists[kWaves][kList];
-  __shared__ Key final_keys[kWaves * SKINNY_MAX_TOP];
+  __shared__ Key groups[kCut];
+  __shared__ Key candidates[kCut * kPer];
   __shared__ Key shared;
   __shared__ Stat parts[kWaves];
+  __shared__ int counts[kWaves];
+  __shared__ int number, found;
   __shared__ int last;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
   const T* x = static_cast<const T*>(a.logits) + r * a.stride;
-  if (threadIdx.x == 0) shared = 0ull;
+  if (threadIdx.x == 0) {
+    shared = 0ull;
+    found = 0;
+  }
   __syncthreads();
 
   // The row's whole 16-byte vectors are split evenly; the elements before and
@@ -261,7 +306,7 @@ __global__ __launch_bounds__(kThreads) void logprobs(const LogprobArgs a) {
   const int per = (vectors + ranges - 1) / ranges;
   const int v0 = range * per < vectors ? range * per : vectors, v1 = v0 + per < vectors ? v0 + per : vectors;
   const u32x4* vec = reinterpret_cast<const u32x4*>(x + head);
-  List list{lists[wave], 0, a.k, 0ull, &shared};
+  List list{lists[wave], 0, a.k, 0ull, -INFINITY, &shared};
   Stat st{-INFINITY, 0.0f, 0.0f};
 
   u32x4 next[kVectors];
@@ -278,29 +323,51 @@ __global__ __launch_bounds__(kThreads) void logprobs(const LogprobArgs a) {
 #pragma unroll
     for (int u = 0; u < kVectors; ++u) L::widen(next[u], e + u * kPer);
     fetch(v + 64 * kVectors);
-    float top = e[0];
+    float most[kVectors];
 #pragma unroll
-    for (int i = 1; i < N; ++i) top = fmaxf(top, e[i]);
+    for (int u = 0; u < kVectors; ++u) {
+      most[u] = e[u * kPer];
+#pragma unroll
+      for (int i = 1; i < kPer; ++i) most[u] = fmaxf(most[u], e[u * kPer + i]);
+    }
+    const float top = fmaxf(most[0], most[1]);
     add(st, e, top);
-    collect(list, e, top, [&](int i) { return head + (v + i / kPer * 64 + lane) * kPer + i % kPer; },
-            [&](int i) { return v + i / kPer * 64 + lane < v1; });
+    collect(list, most, top, [&](int u) { return head + (v + u * 64 + lane) * kPer; },
+            [&](int u) { return v + u * 64 + lane < v1; });
   }
-  if (range == 0 && head + tail > 0) {
+  if (range == 0 && head + tail > 0) {  // groups of one element
     const int col = lane < head ? lane : a.V - tail + (lane - head);
     const bool real = lane < head + tail;
     const float e[1] = {real ? L::at(x + col) : -INFINITY};
     add(st, e, e[0]);
     collect(list, e, e[0], [&](int) { return col; }, [&](int) { return real; });
   }
-  list.cut();
   st = wave_join(st);
-  if (lane == 0) parts[wave] = st;
-  __builtin_amdgcn_wave_barrier();
-  if (lane < a.k) final_keys[wave * a.k + lane] = lane < list.n ? list.keys[lane] : 0ull;
-  __syncthreads();
+  if (lane == 0) {
+    parts[wave] = st;
+    counts[wave] = list.n;
+  }
+  // Their elements that reach the least of k groups; all, if there are fewer.
+  const int ng = merge_lists(lists, counts, a.k, groups, &number);
   st = join(join(parts[0], parts[1]), join(parts[2], parts[3]));
+  float floor = lane < ng ? key_value(groups[lane]) : INFINITY;
+  floor = ng < a.k ? -INFINITY : -lane_63(lanes_greatest(-floor));
+  for (int i0 = 0; i0 < ng * kPer; i0 += kThreads) {
+    const int i = i0 + threadIdx.x;
+    const int col = i < ng * kPer ? key_index(groups[i / kPer]) + i % kPer : 0;
+    const bool whole = col - i % kPer >= head && col - i % kPer < a.V - tail;
+    const bool real = i < ng * kPer && (whole || i % kPer == 0);
+    const float e = real ? L::at(x + col) : NAN;
+    const bool want = e >= floor;
+    const unsigned long long mask = __ballot(want);
+    int at = 0;
+    if (lane == 0 && mask) at = atomicAdd(&found, __popcll(mask));
+    at = __builtin_amdgcn_readfirstlane(at) + lanes_below(mask);
+    if (want) candidates[at] = argmax_key(e, col);
+  }
+  __syncthreads();
   if (a.splits == 1) {
-    finish<L>(a, r, x, st, final_keys, kWaves * a.k);
+    finish<L>(a, r, x, st, candidates, found);
     return;
   }
 
@@ -310,27 +377,18 @@ __global__ __launch_bounds__(kThreads) void logprobs(const LogprobArgs a) {
   // keys' order nor that of the sums depends on the arrivals.
   Key* keys = a.keys + static_cast<size_t>(r) * a.splits * a.k;
   Key* stats = a.stats + static_cast<size_t>(r) * a.splits * 2;
-  if (wave == 0) {
-    Key held[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) held[i] = i * 64 + lane < kWaves * a.k ? final_keys[i * 64 + lane] : 0ull;
-    const Key least = kth_key<2>(held, a.k);
-    list.n = 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) list.push(held[i] >= least && held[i] > 0ull, held[i]);
-    __builtin_amdgcn_wave_barrier();
-    if (lane < a.k) put(keys + split * a.k + lane, lane < list.n ? list.keys[lane] : 0ull);
-    if (lane == 0) {
-      put(stats + split * 2, two(st.m, st.s));
-      put(stats + split * 2 + 1, two(st.t, 0.0f));
-    }
-    __builtin_amdgcn_s_waitcnt(0);
-    if (lane == 0) {
-      unsigned* count = a.sync + static_cast<size_t>(r) * (kSyncLineBytes / 4);
-      const unsigned old = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      last = old == static_cast<unsigned>(a.splits - 1);
-      if (last) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
+  ranked(candidates, found, a.k, [&](int rank, Key key) { put(keys + split * a.k + rank, key); });
+  if (threadIdx.x == 0) {
+    put(stats + split * 2, two(st.m, st.s));
+    put(stats + split * 2 + 1, two(st.t, 0.0f));
+  }
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    unsigned* count = a.sync + static_cast<size_t>(r) * (kSyncLineBytes / 4);
+    const unsigned old = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    last = old == static_cast<unsigned>(a.splits - 1);
+    if (last) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __syncthreads();
   if (!last) return;
@@ -342,17 +400,14 @@ __global__ __launch_bounds__(kThreads) void logprobs(const LogprobArgs a) {
     list.push(key > list.over, key);
     if (list.n > kKeep) list.cut();
   }
-  list.cut();
-  __builtin_amdgcn_wave_barrier();
-  if (lane < a.k) final_keys[wave * a.k + lane] = lane < list.n ? list.keys[lane] : 0ull;
+  if (lane == 0) counts[wave] = list.n;
   st = Stat{-INFINITY, 0.0f, 0.0f};
   for (int i = lane; i < a.splits; i += 64) {
     const Key ms = get(stats + i * 2), t = get(stats + i * 2 + 1);
     st = join(st, Stat{low(ms), high(ms), low(t)});
   }
   st = wave_join(st);
-  __syncthreads();
-  finish<L>(a, r, x, st, final_keys, kWaves * a.k);
+  finish<L>(a, r, x, st, groups, merge_lists(lists, counts, a.k, groups, &number));
 }
 
 // Workgroups per row: enough of them to fill the chip, each with one step of
