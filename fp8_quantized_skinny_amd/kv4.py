@@ -19,39 +19,43 @@ MAX_TOP = 32
 _CACHE = struct.Struct("=QQQiiiiiff4x").pack    # kv4_cache
 _ROWS = struct.Struct("=Qqqq").pack             # kv4_rows
 _TYPES = {}
+_TORCH = None
 
 
 def _torch():
-    import torch
-    if not _TYPES:
+    global _TORCH
+    if _TORCH is None:
+        import torch
         _TYPES.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
-    return torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _is_tensor(t, name):
-    import torch
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
 
 
 def _device(t, name, device):
+    if t.get_device() == device:
+        return
     if not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{device}")
+    raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{device}")
 
 
 def _buffer(t, dtype, shape, name, device):
     """The address of a contiguous device tensor of exactly this type and shape."""
+    if (isinstance(t, _torch().Tensor) and t.get_device() == device and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
+        return t.data_ptr()
     _is_tensor(t, name)
     _device(t, name, device)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _rows(t, name, device):
@@ -89,7 +93,7 @@ def _cache(cache, table, lens, gk, gv, torch, device, names=("cache", "table", "
 
 def _stream(torch, stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())  # current_stream() builds an object
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
