@@ -59,20 +59,37 @@ __device__ __forceinline__ float max_over_rows(float v) {
   return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
 }
 
-// LDS copy of a workgroup's query rows as fp16, row stride D + 8 halves (16
-// bytes off the banks' period).  bf16 rows are scaled by the power of two that
-// brings their greatest value to 2^14 .. 2^15; `factor` undoes it.
-template <int D, int MT, class E>
-__device__ __forceinline__ void stage_queries(const kv4_rows& q, int b, int h, int qg, int G, int R, _Float16* qs,
-                                              float* factor) {
-  constexpr int kPer = D / 8;  // threads per row
-  for (int i = threadIdx.x; i < MT * 16 * kPer; i += kThreads) {
-    const int row = i / kPer, piece = i % kPer;
-    const int r = qg * MT * 16 + row;
-    u32x4 w{0u, 0u, 0u, 0u};
-    if (r < R)
-      w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(q.data) + b * q.sequence + (r / G) * q.row +
-                                          (h * G + r % G) * q.head + piece * 8);
+// A workgroup's query rows: loaded before its keys, since loads arrive in
+// order, then put into LDS as fp16 with a row stride of D + 8 halves (16 bytes
+// off the banks' period).  bf16 rows are scaled by the power of two that brings
+// their greatest value to 2^14 .. 2^15; `factor` undoes it.
+template <int D, int MT>
+struct Queries {
+  static constexpr int kPer = D / 8;  // threads per row
+  static constexpr int kItems = (MT * 16 * kPer + kThreads - 1) / kThreads;
+  static_assert(MT * 16 * kPer % 64 == 0, "whole wavefronts take part in the shuffles");
+  u32x4 loaded[kItems];
+
+  __device__ __forceinline__ void load(const kv4_rows& q, int b, int h, int qg, int G, int R) {
+#pragma unroll
+    for (int n = 0; n < kItems; ++n) {
+      const int i = n * kThreads + threadIdx.x, r = qg * MT * 16 + i / kPer;
+      loaded[n] = u32x4{0u, 0u, 0u, 0u};
+      if (i < MT * 16 * kPer && r < R)
+        loaded[n] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(q.data) + b * q.sequence + (r / G) * q.row +
+                                                    (h * G + r % G) * q.head + i % kPer * 8);
+    }
+  }
+  template <class E>
+  __device__ __forceinline__ void put(_Float16* qs, float* factor) const {
+#pragma unroll
+    for (int n = 0; n < kItems; ++n) {
+      const int i = n * kThreads + threadIdx.x;
+      if (i < MT * 16 * kPer) put_piece<E>(i / kPer, i % kPer, loaded[n], qs, factor);
+    }
+  }
+  template <class E>
+  static __device__ __forceinline__ void put_piece(int row, int piece, u32x4 w, _Float16* qs, float* factor) {
     if constexpr (std::is_same_v<E, BF16>) {
       float amax = 0.0f;
 #pragma unroll
@@ -94,7 +111,7 @@ __device__ __forceinline__ void stage_queries(const kv4_rows& q, int b, int h, i
     }
     *reinterpret_cast<u32x4*>(qs + row * (D + 8) + piece * 8) = w;
   }
-}
+};
 
 // A lane's part of a block: K and V codes and scales.
 template <int D>
@@ -238,7 +255,8 @@ __device__ __forceinline__ Share plan_share(const kv4_cache& c, int QG, int leas
     return s;
   }
   const auto pages = [&](int b) { return b < c.B ? (kv_len(c, b) + kPage - 1) / kPage : 0; };
-  int mine = pages(lane), total = 0;
+  const int held = lane < c.B ? kv_len(c, lane) : 0;  // of the first 64 sequences
+  int mine = (held + kPage - 1) / kPage, total = 0;
   for (int b0 = 0; b0 < c.B; b0 += 64)
     total += __builtin_amdgcn_readlane(wave_scan(b0 ? pages(b0 + lane) : mine), 63);
   int chunk = total / (room - (c.B >> 1)) + 1;
@@ -264,7 +282,7 @@ __device__ __forceinline__ Share plan_share(const kv4_cache& c, int QG, int leas
       s.splits = __builtin_amdgcn_readlane(n, l);
       const int first = __builtin_amdgcn_readlane(upto, l) - s.splits;
       s.first = first * per + hq;
-      s.len = kv_len_uniform(c, s.b);
+      s.len = b0 ? kv_len_uniform(c, s.b) : __builtin_amdgcn_readlane(held, l);
       const int np = (s.len + kPage - 1) / kPage, each = (np + s.splits - 1) / s.splits;
       s.p0 = (at - first) * each;
       s.p1 = s.p0 + each < np ? s.p0 + each : np;
@@ -277,7 +295,9 @@ __device__ __forceinline__ Share plan_share(const kv4_cache& c, int QG, int leas
   return s;
 }
 
-// A page that the table does not name is read as page 0 and lies past every limit.
+// A page that the table does not name is read as page 0 and lies past every
+// limit: slots of a table are fewer than kNowhere, and kNowhere + 63 is an int.
+constexpr int kNowhere = 0x7FFFFFC0;
 struct Page {
   const uint8_t* block;
   int first;
@@ -287,7 +307,7 @@ __device__ __forceinline__ Page page_of(const kv4_cache& c, int id, int page, in
   const bool named = static_cast<unsigned>(id) < static_cast<unsigned>(c.pages);
   return Page{static_cast<const uint8_t*>(c.data) +
                   (static_cast<size_t>(named ? id : 0) * c.Hk + h) * KvBlock<D>::kBytes,
-              named ? page * kPage : 0x3FFFFFFF};
+              named ? page * kPage : kNowhere};
 }
 
 // Workgroups per CU that a wavefront's registers allow.
@@ -313,6 +333,8 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
     a.split[(b * a.c.Hk + h) * a.QG + qg] = int2{sh.first, sh.splits};
   const int32_t* table = a.c.table + static_cast<size_t>(b) * a.c.width;
   int page = sh.p0 + wave;
+  Queries<D, MT> q;
+  q.load(a.q, b, h, qg, a.G, R);
   KRegs<D> k;
   VRegs<D> v;
   Page now{nullptr, 0}, next{nullptr, 0};
@@ -323,7 +345,7 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
     k.load(now.block, lane);
     v.load(now.block, lane);
   }
-  stage_queries<D, MT, E>(a.q, b, h, qg, a.G, R, qs, factor);
+  q.template put<E>(qs, factor);
   if (threadIdx.x < MT * 16) {
     const int r = qg * MT * 16 + threadIdx.x;
     limits[threadIdx.x] = r < R ? len - (a.T - 1 - r / a.G) : 0;
@@ -371,7 +393,7 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (!kLateKeys) k.load(next.block, lane);
-    if (first + kPage > len - (a.T - 1)) {  // some row does not see the whole page
+    if (first > len - (a.T - 1) - kPage) {  // some row does not see the whole page
       int limit[MT];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) limit[mt] = limits[mt * 16 + c];
@@ -598,68 +620,81 @@ __global__ __launch_bounds__(kThreads) void add_weights(const WeightArgs a) {
   const int h = i % a.c.Hk, b = i / a.c.Hk;
   const int len = kv_len_uniform(a.c, b), R = a.T * a.G;
   const int p0 = chunk * a.per, p1 = p0 + a.per < a.c.width ? p0 + a.per : a.c.width;
+  const int used = (len + kPage - 1) / kPage, end = used < p1 ? used : p1;  // pages from `end` on only get zeros
   const float* acc = a.acc + (static_cast<size_t>(b) * a.c.Hk + h) * a.c.width * kPage;
   float* out = a.out + (static_cast<size_t>(b) * a.c.Hk + h) * a.c.width * kPage;
   const int32_t* table = a.c.table + static_cast<size_t>(b) * a.c.width;
+  for (int page = (end > p0 ? end : p0) + wave; page < p1; page += kWaves) out[page * kPage + lane] = 0.0f;
+  if (p0 >= end) return;
   // Rows in groups of MT * 16; the first group also brings acc along.
   for (int qg = 0; qg * MT * 16 < R; ++qg) {
+    Queries<D, MT> q;
+    q.load(a.q, b, h, qg, a.G, R);
+    KRegs<D> k;
+    Page now{nullptr, 0};
+    if (p0 + wave < end) {
+      now = page_of<D>(a.c, uniform_load(table, p0 + wave), p0 + wave, h);
+      k.load(now.block, lane);
+    }
     __syncthreads();
-    if (p0 * kPage < len) stage_queries<D, MT, E>(a.q, b, h, qg, a.G, R, qs, factor);
-    __syncthreads();
-    float cm[MT][4], sub[MT][4];
+    q.template put<E>(qs, factor);
+    float sub[MT][4];
     int limit[MT][4];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int local = mt * 16 + 4 * g + e, r = qg * MT * 16 + local;
+        const int r = qg * MT * 16 + mt * 16 + 4 * g + e;
         limit[mt][e] = r < R ? len - (a.T - 1 - r / a.G) : 0;
-        cm[mt][e] = fmaxf(a.scale * a.c.gk * kLog2e * factor[local], kMinNormal);
         sub[mt][e] = r < R ? a.lse[(static_cast<size_t>(b) * a.T + r / a.G) * a.Hq + h * a.G + r % a.G] * kLog2e : 0.0f;
       }
-    for (int page = p0 + wave; page < p1; page += kWaves) {
-      const int first = page * kPage, slot = first + lane;
-      float sum = slot < len ? (qg == 0 ? acc[slot] : out[slot]) : 0.0f;
-      const uint8_t* block = first < len ? kv_block<D>(a.c, uniform_load(table, page), h) : nullptr;
-      if (block) {
-        KRegs<D> k;
-        k.load(block, lane);
-        f32x4 s[4][MT];
+    __syncthreads();
+    float cm[MT][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) s[j][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int e = 0; e < 4; ++e) cm[mt][e] = fmaxf(a.scale * a.c.gk * kLog2e * factor[mt * 16 + 4 * g + e], kMinNormal);
+    for (int page = p0 + wave; page < end; page += kWaves) {
+      const int first = now.first, slot = page * kPage + lane;
+      const float before = slot < len ? (qg == 0 ? acc[slot] : out[slot]) : 0.0f;
+      const bool more = page + kWaves < end;
+      if (more) now = page_of<D>(a.c, uniform_load(table, page + kWaves), page + kWaves, h);
+      f32x4 s[4][MT];
 #pragma unroll
-        for (int step = 0; step < D / 32; ++step) {
-          f16x8 qf[MT];
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-            qf[mt] = *reinterpret_cast<const f16x8*>(qs + (mt * 16 + c) * kRow + g * (D / 4) + step * 8);
+        for (int mt = 0; mt < MT; ++mt) s[j][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const f16x8 kf = k.frag(j, step);
+      for (int step = 0; step < D / 32; ++step) {
+        f16x8 qf[MT];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              s[j][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qf[mt], kf, s[j][mt], 0, 0, 0);
-          }
-        }
-        float mine = 0.0f;
+        for (int mt = 0; mt < MT; ++mt)
+          qf[mt] = *reinterpret_cast<const f16x8*>(qs + (mt * 16 + c) * kRow + g * (D / 4) + step * 8);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float w = 0.0f;
+          const f16x8 kf = k.frag(j, step);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][mt][e], cm[mt][e], -sub[mt][e]));
-              w += first + 16 * j + c < limit[mt][e] ? p : 0.0f;
-            }
-          w = sum_over_rows(w);
-          mine = j == g ? w : mine;  // lane 16 g + c keeps token 16 g + c
+            s[j][mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qf[mt], kf, s[j][mt], 0, 0, 0);
         }
-        if (slot < len) sum += mine;
+        __builtin_amdgcn_sched_barrier(0);  // as in attend
       }
-      out[slot] = sum;
+      if (more) k.load(now.block, lane);
+      float mine = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float w = 0.0f;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][mt][e], cm[mt][e], -sub[mt][e]));
+            w += first + 16 * j + c < limit[mt][e] ? p : 0.0f;
+          }
+        w = sum_over_rows(w);
+        mine = j == g ? w : mine;  // lane 16 g + c keeps token 16 g + c
+      }
+      out[slot] = slot < len ? before + mine : 0.0f;
     }
   }
 }
@@ -668,17 +703,21 @@ __global__ __launch_bounds__(kThreads) void add_weights(const WeightArgs a) {
 // D / 4 of them for its sums and 16 for a page's scores.
 constexpr int max_tiles(int D) { return D == 256 ? 2 : 3; }
 
-template <int D, class F>
+// The weights have no sums of values to hold.
+constexpr int kWeightTiles = 3;
+
+template <int MOST, class F>
 void by_tiles(int tiles, F f) {
   if (tiles == 1) f(std::integral_constant<int, 1>());
   else if (tiles == 2) f(std::integral_constant<int, 2>());
-  else if constexpr (max_tiles(D) > 2) f(std::integral_constant<int, 3>());
+  else if constexpr (MOST > 2) f(std::integral_constant<int, 3>());
 }
 
-template <class F>
-hipError_t by_shape(int D, int type, int tiles, F f) {
+// f(head size, tiles, type); `most` gives the most tiles of a head size.
+template <class M, class F>
+hipError_t by_shape(int D, int type, int tiles, M most, F f) {
   const auto run = [&](auto d) {
-    by_tiles<d()>(tiles, [&](auto mt) {
+    by_tiles<most(d())>(tiles, [&](auto mt) {
       if (type == SKINNY_F16) f(d, mt, F16());
       else f(d, mt, BF16());
     });
@@ -734,7 +773,7 @@ hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type,
     a.split = reinterpret_cast<int2*>(ws + p.split_off);
   }
   const unsigned segments = static_cast<unsigned>(c.B * c.Hk * p.QG);
-  return by_shape(c.D, type, p.MT, [&](auto d, auto mt, auto e) {
+  return by_shape(c.D, type, p.MT, [](int D) constexpr { return max_tiles(D); }, [&](auto d, auto mt, auto e) {
     attend<d(), mt(), decltype(e)><<<dim3(static_cast<unsigned>(p.grid)), kThreads, 0, stream>>>(a);
     if (p.split)
       attend_join<d(), mt(), decltype(e)><<<dim3(segments * (mt() * 16)), kThreads, 0, stream>>>(a);
@@ -743,14 +782,14 @@ hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type,
 
 hipError_t launch_kv4_weights(const kv4_cache& c, const kv4_rows& q, int type, int T, int Hq, float scale,
                               const float* lse, const float* acc, float* acc_out, hipStream_t stream) {
-  const int G = Hq / c.Hk, all = (T * G + 15) / 16, tiles = all < max_tiles(c.D) ? all : max_tiles(c.D);
+  const int G = Hq / c.Hk, all = (T * G + 15) / 16, tiles = all < kWeightTiles ? all : kWeightTiles;
   const int64_t pages = static_cast<int64_t>(c.B) * c.Hk * c.width;
   int64_t per = pages / 1024;
   per = per < kWaves ? kWaves : (per > 16 ? 16 : per);
   WeightArgs a{c, q, lse, acc, acc_out, T, Hq, G, static_cast<int>(per), scale};
   const int64_t groups = (c.width + per - 1) / per;
   const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(c.B) * c.Hk * groups));
-  return by_shape(c.D, type, tiles, [&](auto d, auto mt, auto e) {
+  return by_shape(c.D, type, tiles, [](int) constexpr { return kWeightTiles; }, [&](auto d, auto mt, auto e) {
     add_weights<d(), mt(), decltype(e)><<<grid, kThreads, 0, stream>>>(a);
   });
 }
