@@ -82,9 +82,24 @@ def lib():
         except ImportError:       # host-only use (packing, quantizing) without torch
             pass
         if not os.path.exists(_build.LIB):
-            _build.build()
+            _build.build_library()
         _LIB = _declare(ctypes.CDLL(_build.LIB))
     return _LIB
+
+
+_NATIVE = None
+
+
+def native():
+    """The extension module that checks torch tensors and makes the calls of kv4.py."""
+    global _NATIVE
+    if _NATIVE is None:
+        lib()
+        if not os.path.exists(_build.BINDING):
+            _build.build_binding()
+        from . import _binding
+        _NATIVE = _binding
+    return _NATIVE
 
 
 EXPORTED = ("nvfp4_pack", "nvfp4_gemm", "fp8_gemm", "lm_head_gemm_argmax", "nvfp4_quantize",

@@ -1,4 +1,5 @@
-"""Build libskinny.so in-tree with hipcc for gfx950.
+"""Build libskinny.so in-tree with hipcc for gfx950, and _binding.so, the Python
+extension that checks torch tensors for some of its calls, with the host compiler.
 
     python -m fp8_quantized_skinny_amd.build
 
@@ -21,6 +22,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libskinny.so")
+BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["host.cpp", "nvfp4_gemm.hip", "fp8_gemm.hip", "reduce.hip", "probe.hip", "noalloc.hip",
            "kv4_host.cpp", "kv4_cache.hip", "kv4_attention.hip", "logprobs.hip"]
 ARCH = "gfx950"
@@ -37,6 +39,13 @@ def hipcc():
 
 
 def build(verbose=False):
+    """Build libskinny.so and _binding.so; returns the library path."""
+    build_library(verbose)
+    build_binding(verbose)
+    return LIB
+
+
+def build_library(verbose=False):
     """Compile every source and link libskinny.so; returns the library path."""
     objdir = os.path.join(PKG, "_build")
     os.makedirs(objdir, exist_ok=True)
@@ -57,6 +66,24 @@ def build(verbose=False):
     _run([hipcc(), "-shared", "-fPIC", "-pthread", f"--offload-arch={ARCH}", *objs, "-o", tmp], verbose)
     os.replace(tmp, LIB)
     return LIB
+
+
+def build_binding(verbose=False):
+    """Compile csrc/binding.cpp against torch's headers; it finds libskinny.so beside itself."""
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    include = [INCLUDE, os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               os.path.join(rocm, "include"), sysconfig.get_paths()["include"]]
+    tmp = BINDING + ".tmp"
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+          *[f"-I{i}" if i == INCLUDE else f"-isystem{i}" for i in include], os.path.join(CSRC, "binding.cpp"), "-o", tmp,
+          "-L" + PKG, "-l:libskinny.so", "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(home, "lib"),
+          "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"], verbose)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def scratch_per_kernel(report):
