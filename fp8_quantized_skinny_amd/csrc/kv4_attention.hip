@@ -19,8 +19,8 @@
 // at positions c * D/16 ...
 #include <hip/hip_runtime.h>
 
-#include "internal.h"
 #include "kv4.cuh"
+#include "kv4_internal.h"
 
 namespace skinny {
 namespace {

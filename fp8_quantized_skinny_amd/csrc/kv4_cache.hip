@@ -4,8 +4,8 @@
 
 #include <type_traits>
 
-#include "internal.h"
 #include "kv4.cuh"
+#include "kv4_internal.h"
 
 namespace skinny {
 namespace {
@@ -272,8 +272,8 @@ __device__ __forceinline__ int2 block_scan(int2 v, int2* tmp, int2& total) {
 
 // One workgroup per sequence and head finds the key of the last slot kept by
 // narrowing a range of keys: bins of equal width over the range's keys, the
-// bin that holds the wanted rank, and again within it until it is one key (at
-// most three times for 32-bit keys).  Equal-width bins between the least and
+// bin that holds the wanted rank, and again within it until it is one key or
+// all of its keys stay (at most three times for 32-bit keys).  Equal-width bins between the least and
 // the greatest key spread weights that differ by factors over many bins.
 //
 // The keys lie in LDS, where a thread finds those that it put there itself,
@@ -281,15 +281,15 @@ __device__ __forceinline__ int2 block_scan(int2 v, int2* tmp, int2& total) {
 // sequences again, 32768 at a time, in each of the passes.  The loops stay
 // short: with the keys in registers instead, the unrolled passes are 50 KB of
 // code that runs once, and fetching it took longer than the work.  16
-// sequences x 4 heads of 20000 .. 32768 slots, keeping 8192: 29 us (91 with a
-// run of slots per thread, read four times over); one of 4133: 13 us (21).
+// sequences x 4 heads of 20000 .. 32768 slots, keeping 8192: 27 us (91 with a
+// run of slots per thread, read four times over); one of 4133: 11 us (21).
 __global__ __launch_bounds__(kSelectThreads) void select_slots(const kv4_cache c, const float* acc, int dst_width,
                                                                int32_t* kept, int32_t* new_lens, float* new_acc,
                                                                int keep, int sinks, int recent) {
   __shared__ int bins[kBins];
   __shared__ int2 tmp[kSelectWaves];
   __shared__ uint32_t range[2];
-  __shared__ int found[2];
+  __shared__ int found[2][3];
   __shared__ int2 count[kRows * kSelectWaves];  // of a wavefront's 256 slots: those above the last key, those equal to it
   const unsigned tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;  // slots of a tile may pass 2^31
   const int h = blockIdx.x % c.Hk, b = blockIdx.x / c.Hk;
@@ -357,6 +357,7 @@ __global__ __launch_bounds__(kSelectThreads) void select_slots(const kv4_cache c
     range[0] = kSure;
     range[1] = 0u;
   }
+  for (unsigned i = tid; i < kBins; i += kSelectThreads) bins[i] = 0;
   __syncthreads();
   uint32_t lo = kSure, hi = 0u;
   each([&](uint32_t k) __attribute__((always_inline)) {
@@ -374,36 +375,39 @@ __global__ __launch_bounds__(kSelectThreads) void select_slots(const kv4_cache c
   __syncthreads();
   lo = range[0];
   hi = range[1];
-  while (need > 0 && lo < hi) {
+  bool whole = false;  // every key from lo on stays
+  for (int pass = 0; need > 0 && lo < hi && !whole; ++pass) {
     int shift = 0;
     while (((hi - lo) >> shift) >= kBins) ++shift;
-    for (unsigned i = tid; i < kBins; i += kSelectThreads) bins[i] = 0;
-    __syncthreads();
     each([&](uint32_t k) __attribute__((always_inline)) {
       if (k - lo <= hi - lo) atomicAdd(&bins[(k - lo) >> shift], 1);
     });
     __syncthreads();
-    // Bins from the top: thread t has bins kBins-1-2t and kBins-2-2t.
+    // Bins from the top: thread t has bins kBins-1-2t and kBins-2-2t, and clears them for the next pass.
     const int top = kBins - 1 - 2 * static_cast<int>(tid), a = bins[top], d = bins[top - 1];
+    bins[top] = bins[top - 1] = 0;
     int2 total;
     const int above = block_scan(int2{a + d, 0}, tmp, total).x;
+    int* at = found[pass % 2];  // the bin, the keys above it, and its own
     if (above < need && need <= above + a + d) {
       const bool first = need <= above + a;
-      found[0] = first ? top : top - 1;
-      found[1] = first ? above : above + a;
+      at[0] = first ? top : top - 1;
+      at[1] = first ? above : above + a;
+      at[2] = first ? a : d;
     }
     __syncthreads();
-    need -= found[1];
-    const uint32_t base = lo + (static_cast<uint32_t>(found[0]) << shift);
+    need -= at[1];
+    whole = need == at[2];
+    const uint32_t base = lo + (static_cast<uint32_t>(at[0]) << shift);
     const uint32_t last = base + ((1u << shift) - 1u);
     lo = base;
     hi = last < base || last > hi ? hi : last;
-    __syncthreads();
     if (shift == 0) hi = lo;
   }
-  // Every key above lo stays, and `need` of those equal to it, the lowest
+  // Every key above the edge stays, and `need` of those equal to it, the lowest
   // slots: a slot's place is the number of slots before it that stay.
-  const uint32_t edge = need > 0 ? lo : kSure - 1u;
+  if (whole) need = 0;
+  const uint32_t edge = whole ? lo - 1u : (need > 0 ? lo : kSure - 1u);
   int2 before{0, 0};
   for (unsigned base = 0;; base += kTileSlots) {
     if (n > kTileSlots) load(base);

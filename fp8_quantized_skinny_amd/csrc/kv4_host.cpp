@@ -2,7 +2,7 @@
 // argument checks before any HIP call.
 #include <cmath>
 
-#include "internal.h"
+#include "kv4_internal.h"
 #include "skinny.h"
 
 using namespace skinny;

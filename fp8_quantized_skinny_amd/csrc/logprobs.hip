@@ -15,8 +15,8 @@
 // has something to add); the groups that are left at the end are read again.
 #include <hip/hip_runtime.h>
 
-#include "internal.h"
 #include "kv4.cuh"
+#include "kv4_internal.h"
 
 namespace skinny {
 namespace {
