@@ -549,7 +549,7 @@ __global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a) {
   constexpr int kPer = D / 4, kSets = kThreads / kPer, kBatch = 8;
   __shared__ f32x4 sums[kSets][kPer];
   __shared__ float2 stats[kSets];
-  const int segment = blockIdx.x / (MT * 16), local = blockIdx.x % (MT * 16);
+  const int segment = blockIdx.x, local = blockIdx.y;
   const int qg = segment % a.QG, h = segment / a.QG % a.c.Hk, b = segment / a.QG / a.c.Hk, stride = a.c.Hk * a.QG;
   const int r = qg * MT * 16 + local;
   if (r >= a.T * a.G) return;
@@ -776,7 +776,7 @@ hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type,
   return by_shape(c.D, type, p.MT, [](int D) constexpr { return max_tiles(D); }, [&](auto d, auto mt, auto e) {
     attend<d(), mt(), decltype(e)><<<dim3(static_cast<unsigned>(p.grid)), kThreads, 0, stream>>>(a);
     if (p.split)
-      attend_join<d(), mt(), decltype(e)><<<dim3(segments * (mt() * 16)), kThreads, 0, stream>>>(a);
+      attend_join<d(), mt(), decltype(e)><<<dim3(segments, mt() * 16), kThreads, 0, stream>>>(a);
   });
 }
 

@@ -11,7 +11,8 @@ namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 int launch_status(hipError_t e) { return e == hipSuccess ? SKINNY_OK : SKINNY_EHIP; }
-bool fits_grid(int64_t groups) { return groups < (int64_t{1} << 31); }
+// A grid has fewer than 2^32 threads in a dimension.
+bool fits_grid(int64_t groups, int threads = 256) { return groups < (int64_t{1} << 32) / threads; }
 
 int check_shape(int B, int Hk, int D, int width) {
   if (B < 1 || B > 65536 || Hk < 1 || Hk > 1024) return SKINNY_ESHAPE;
@@ -99,7 +100,7 @@ int kv4_attention(const kv4_cache* cache, const kv4_rows* q, int type, int T, in
   if (!out) return SKINNY_EINVAL;
   if (!aligned(out, 16) || !aligned(lse, 4)) return SKINNY_EALIGN;
   const AttendPlan plan = kv4_attend_plan(cache->B, T, Hq, cache->Hk, cache->D, cache->width);
-  if (!fits_grid(plan.grid)) return SKINNY_ESHAPE;
+  if (!fits_grid(plan.grid) || !fits_grid(static_cast<int64_t>(cache->B) * cache->Hk * plan.QG)) return SKINNY_ESHAPE;
   const size_t need = plan.total;
   if (need) {
     if (!workspace) return SKINNY_EINVAL;
@@ -115,7 +116,8 @@ int kv4_attention_weights(const kv4_cache* cache, const kv4_rows* q, int type, i
   if (s) return s;
   if (!lse || !acc || !acc_out) return SKINNY_EINVAL;
   if (!aligned(lse, 4) || !aligned(acc, 16) || !aligned(acc_out, 16)) return SKINNY_EALIGN;
-  if (!fits_grid(static_cast<int64_t>(cache->B) * cache->Hk * cache->width)) return SKINNY_ESHAPE;
+  // A workgroup takes 16 pages of a head where there are many.
+  if (!fits_grid(static_cast<int64_t>(cache->B) * cache->Hk * ((cache->width + 15) / 16))) return SKINNY_ESHAPE;
   return launch_status(launch_kv4_weights(*cache, *q, type, T, Hq, scale, lse, acc, acc_out, stream));
 }
 
@@ -130,6 +132,7 @@ int kv4_evict(const kv4_cache* cache, const float* acc, const kv4_cache* dst, in
   if (keep < 1 || sinks < 0 || recent < 0 || sinks > keep || recent > keep - sinks) return SKINNY_EINVAL;
   if (keep > static_cast<int64_t>(dst->width) * SKINNY_KV_PAGE) return SKINNY_ESIZE;
   if (!aligned(acc, 16) || !aligned(kept, 4) || !aligned(new_lens, 4) || !aligned(new_acc, 16)) return SKINNY_EALIGN;
+  if (!fits_grid(static_cast<int64_t>(cache->B) * cache->Hk, 1024)) return SKINNY_ESHAPE;
   if (!fits_grid(static_cast<int64_t>(cache->B) * kv4_row_pages(keep) * cache->Hk)) return SKINNY_ESHAPE;
   return launch_status(
       launch_kv4_evict(*cache, acc, *dst, kept, new_lens, new_acc, keep, sinks, recent, stream));
