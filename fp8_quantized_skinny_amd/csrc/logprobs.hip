@@ -13,6 +13,13 @@
 // long, and the threshold, which the workgroup's wavefronts share, rises.  The
 // pass pays one comparison per load for it (and a few operations where a lane
 // has something to add); the groups that are left at the end are read again.
+//
+// Bound by the VALU where there are many rows (12 operations an element, seven
+// of them for the sums): 2048 rows of 151936 bf16 logits, 20 alternatives,
+// take 116 us, 5.4 TB/s.  Collecting every element above the threshold took
+// 240 us; 131 with loads behind a branch, each waited for at once.  Eight such
+// rows of fp16 take 11 us, which is latency: a load, two cuts, and the meeting
+// of 38 workgroups per row.
 #include <hip/hip_runtime.h>
 
 #include "kv4.cuh"
@@ -28,10 +35,10 @@ constexpr int kThreads = 64 * kWaves;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kVectors = 2;                      // 16-byte loads of a lane per step
 constexpr int kMost = kVectors * 8;              // elements of a lane per step
-constexpr int kCut = 64;                         // most keys that a cut leaves
-constexpr int kKeep = 128;                       // keys at which a list is cut back
+constexpr int kSpare = 8;                        // most keys that a cut leaves besides k
+constexpr int kKeep = 64;                        // keys at which a list is cut back
 constexpr int kList = kKeep + 64 * kVectors;     // a step adds kVectors keys per lane at most
-static_assert(SKINNY_MAX_TOP <= kCut, "a cut leaves k keys at least");
+static_assert(SKINNY_MAX_TOP + kSpare < kKeep, "a cut makes room");
 
 struct F32 {
   using T = float;
@@ -97,8 +104,8 @@ __device__ __forceinline__ float key_value(Key key) {
 }
 __device__ __forceinline__ int key_index(Key key) { return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(key)); }
 
-// A value that k .. kCut of the wavefront's keys (N per lane, all different or
-// 0) reach, by bits from the top; 0 if fewer than k keys are not 0.
+// A value that k .. k + kSpare of the wavefront's keys (N per lane, all
+// different or 0) reach, by bits from the top; 0 if fewer than k are not 0.
 template <int N>
 __device__ __forceinline__ Key kth_key(const Key (&key)[N], int k) {
   Key at = 0ull;
@@ -109,7 +116,7 @@ __device__ __forceinline__ Key kth_key(const Key (&key)[N], int k) {
     for (int i = 0; i < N; ++i) n += __popcll(__ballot(key[i] >= next));
     if (n >= k) {
       at = next;
-      if (n <= kCut) break;
+      if (n <= k + kSpare) break;
     }
   }
   return at;
@@ -135,10 +142,13 @@ struct List {
     if (want) keys[n + lanes_below(mask)] = key;
     n += __popcll(mask);
   }
-  // Cuts the list back to at most kCut keys, the k greatest among them.
+  // Cuts the list back to at most k + kSpare keys, the k greatest among them.
   __device__ __forceinline__ void cut() {
-    if (n <= kCut) return;
-    constexpr int N = kList / 64;
+    if (n <= 128) cut_held<2>();
+    else cut_held<kList / 64>();
+  }
+  template <int N>
+  __device__ __forceinline__ void cut_held() {
     const int lane = threadIdx.x & 63;
     __builtin_amdgcn_wave_barrier();
     Key held[N];
@@ -160,9 +170,10 @@ struct List {
 template <int U, class At, class Real>
 __device__ __forceinline__ void collect(List& list, const float (&most)[U], float top, At at, Real real) {
   if (!__any(top >= list.floor)) return;
-  list.raise(*static_cast<volatile Key*>(list.shared));
+  list.raise(__hip_atomic_load(list.shared, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP));
 #pragma unroll
   for (int u = 0; u < U; ++u) {
+    if (!__any(most[u] >= list.floor)) continue;
     const Key key = argmax_key(most[u], at(u));  // 0 if all are NaN
     list.push(real(u) && key > list.over, key);
   }
@@ -213,8 +224,8 @@ __device__ __forceinline__ Stat wave_join(Stat st) {
   return Stat{m, lane_63(lanes_sum(st.s)), lane_63(lanes_sum(st.t))};
 }
 
-// The workgroup's lists in one: at most kCut keys, the k greatest of all among
-// them, in `out`; returns their number.  A barrier comes first and last.
+// The workgroup's lists in one: at most k + kSpare keys, the k greatest of all
+// among them, in `out`; returns their number.  A barrier comes first and last.
 __device__ __forceinline__ int merge_lists(const Key (*lists)[kList], const int* counts, int k, Key* out, int* number) {
   __syncthreads();
   if (threadIdx.x < 64) {
@@ -281,14 +292,14 @@ __global__ __launch_bounds__(kThreads) void logprobs(const LogprobArgs a) {
   using T = typename L::T;
   constexpr int kPer = L::kPer, N = kVectors * kPer;
   __shared__ Key lists[kWaves][kList];
-  __shared__ Key groups[kCut];
-  __shared__ Key candidates[kCut * kPer];
+  __shared__ Key groups[kKeep];
+  __shared__ Key candidates[kKeep * kPer];
   __shared__ Key shared;
   __shared__ Stat parts[kWaves];
   __shared__ int counts[kWaves];
   __shared__ int number, found;
   __shared__ int last;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
   const T* x = static_cast<const T*>(a.logits) + r * a.stride;
   if (threadIdx.x == 0) {
@@ -309,23 +320,27 @@ __global__ __launch_bounds__(kThreads) void logprobs(const LogprobArgs a) {
   List list{lists[wave], 0, a.k, 0ull, -INFINITY, &shared};
   Stat st{-INFINITY, 0.0f, 0.0f};
 
-  u32x4 next[kVectors];
-  const auto fetch = [&](int v) {
+  // Two steps' loads alternate, so that one is in flight while the other is
+  // used; both are unconditional (past the range's end the last vector again),
+  // since a branch around a load makes the compiler wait for it at once.
+  constexpr int kStep = 64 * kVectors;
+  const auto fetch = [&](int v, u32x4 (&to)[kVectors]) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < kVectors; ++u) {
       const int i = v + u * 64 + lane;
-      next[u] = i < v1 ? load16(vec + i) : u32x4{L::kNone, L::kNone, L::kNone, L::kNone};
+      to[u] = load16(vec + (i < v1 ? i : v1 - 1));
     }
   };
-  fetch(v0);
-  for (int v = v0; v < v1; v += 64 * kVectors) {
-    float e[N];
+  const auto use = [&](int v, u32x4 (&from)[kVectors]) __attribute__((always_inline)) {
+    if (v + kStep > v1) {
 #pragma unroll
-    for (int u = 0; u < kVectors; ++u) L::widen(next[u], e + u * kPer);
-    fetch(v + 64 * kVectors);
-    float most[kVectors];
+      for (int u = 0; u < kVectors; ++u)
+        if (v + u * 64 + lane >= v1) from[u] = u32x4{L::kNone, L::kNone, L::kNone, L::kNone};
+    }
+    float e[N], most[kVectors];
 #pragma unroll
     for (int u = 0; u < kVectors; ++u) {
+      L::widen(from[u], e + u * kPer);
       most[u] = e[u * kPer];
 #pragma unroll
       for (int i = 1; i < kPer; ++i) most[u] = fmaxf(most[u], e[u * kPer + i]);
@@ -334,6 +349,17 @@ __global__ __launch_bounds__(kThreads) void logprobs(const LogprobArgs a) {
     add(st, e, top);
     collect(list, most, top, [&](int u) { return head + (v + u * 64 + lane) * kPer; },
             [&](int u) { return v + u * 64 + lane < v1; });
+  };
+  if (v0 < v1) {
+    u32x4 one[kVectors], two[kVectors];
+    fetch(v0, one);
+    for (int v = v0; v < v1; v += 2 * kStep) {
+      fetch(v + kStep, two);
+      use(v, one);
+      if (v + kStep >= v1) break;
+      fetch(v + 2 * kStep, one);
+      use(v + kStep, two);
+    }
   }
   if (range == 0 && head + tail > 0) {  // groups of one element
     const int col = lane < head ? lane : a.V - tail + (lane - head);
