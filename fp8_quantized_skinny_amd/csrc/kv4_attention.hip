@@ -310,9 +310,19 @@ __device__ __forceinline__ Page page_of(const kv4_cache& c, int id, int page, in
               named ? page * kPage : kNowhere};
 }
 
-// Workgroups per CU that a wavefront's registers allow.
+// Workgroups per CU that a wavefront's registers allow.  More was slower where
+// it could be had: four instead of three with one tile at D = 128, for which
+// the keys arrive late, 71 against 67 us (16 sequences of 30000 .. 32768 tokens,
+// 12 rows a head); two instead of one with two tiles at D = 256, 27 against 26.
 constexpr int attend_per_cu(int D, int MT) { return D == 256 && MT == 2 ? 1 : (D / 64 * MT <= 2 ? 3 : 2); }
 
+// What bounds it: with one tile of queries, memory (16 sequences of 30000 ..
+// 32768 tokens, four heads of 128: 290 MB in 67 us, 4.3 TB/s, where a large copy
+// moves 4.7); with three, memory and the widening and softmax about equally
+// (eight sequences of 120000 .. 131072 tokens: 578 MB and 99 GFLOP in 148 us; the
+// VALU is busy for 57% of the cycles and the matrix unit for 28%); short
+// sequences, latency: of one sequence of 8197 tokens' 16 us a page takes 2.6
+// and the joining of four wavefronts' sums 3.
 template <int D, int MT, class E>
 __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const AttendArgs a) {
   constexpr int DB = D / 16;
@@ -597,6 +607,10 @@ __global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a) {
 // The scores again, from the keys alone, in the other orientation (queries as
 // rows of the result): a lane's column is its token, and the sum over a head's
 // rows is a sum of its own values and of four lanes.
+// The log-sum is known only when a row's last share is done, so the keys are
+// read twice; keeping the scores instead would move 48 bytes a token and head
+// each way for 12 rows, the keys are 72.  Bound by memory: 16 sequences of 30000
+// .. 32768 tokens, four heads of 128, 161 MB in 36 us (4.5 TB/s).
 struct WeightArgs {
   kv4_cache c;
   kv4_rows q;
