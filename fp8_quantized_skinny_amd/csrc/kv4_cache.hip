@@ -196,8 +196,9 @@ __device__ __forceinline__ u32x4 held8(uint32_t codes, uint32_t scale, float g) 
 
 // One workgroup per sequence, head and 64 rows of the output, whose slots lie
 // in two pages at most; a thread takes eight values, so that neighbours' loads
-// and stores are contiguous.  Bound by memory, its writes above all: 16 x 8192
-// tokens, four heads of 128, 343 MB in 76 us (4.5 TB/s).
+// and stores are contiguous.  Bound by memory, its writes above all, which go
+// past the caches: 16 x 8192 tokens, four heads of 128, 268 MB written and 75 MB
+// read in 55 us after the eviction that wrote the pages (76 with ordinary stores).
 template <int D, class E>
 __global__ __launch_bounds__(kThreads) void read_rows(const kv4_cache c, uint16_t* k, uint16_t* v, int n, int np) {
   constexpr int P = D / 8, kItems = kPage * P * 2 / kThreads, kBatch = kItems < 8 ? kItems : 8;
@@ -235,7 +236,7 @@ __global__ __launch_bounds__(kThreads) void read_rows(const kv4_cache c, uint16_
       const bool isv = n0 + u >= kItems / 2;
       if (row0 + r >= n) continue;
       uint16_t* dst = (isv ? v : k) + ((static_cast<size_t>(b) * n + row0 + r) * c.Hk + h) * D + piece * 8;
-      *reinterpret_cast<u32x4*>(dst) = held8<E>(codes[u], scale[u], isv ? c.gv : c.gk);
+      __builtin_nontemporal_store(held8<E>(codes[u], scale[u], isv ? c.gv : c.gk), reinterpret_cast<u32x4*>(dst));
     }
   }
 }
@@ -461,10 +462,13 @@ __global__ __launch_bounds__(kSelectThreads) void select_slots(const kv4_cache c
 // into LDS, all loads in flight at once, and leave as one block.  Neighbours
 // among the kept slots share lines of the source, so each load's lanes are
 // chosen to meet in them: 64 tokens for one piece of K, and of the scales, and
-// four tokens for the whole of V, whose 16 pieces lie in two lines.  Bound by
-// memory: keeping a third of the slots touches nearly every line of the
-// source, so 16 sequences x 4 heads x 8192 slots kept of 20000 .. 32768 read
-// 232 MB and write 75 MB, in 94 us.
+// four tokens for the whole of V, whose 16 pieces lie in two lines.  Codes of
+// the source are loaded non-temporally: they are done with, and what is written
+// here is read next.  Bound by memory: keeping a third of the slots touches
+// nearly every line of the source, so 16 sequences x 4 heads x 8192 slots kept
+// of 20000 .. 32768 read 232 MB and write 75 MB, in 58 us (94 with the caches'
+// own order; 64, and 10 more for the reading that follows, with the stores
+// non-temporal too).
 template <int D>
 __global__ __launch_bounds__(kThreads) void copy_kept(const kv4_cache c, const kv4_cache dst, const int32_t* kept,
                                                       int keep, int np) {
@@ -500,7 +504,7 @@ __global__ __launch_bounds__(kThreads) void copy_kept(const kv4_cache c, const k
   if (block) {
 #pragma unroll
     for (int i = 0; i < kKPieces; ++i)
-      kc[i] = *reinterpret_cast<const KPiece*>(block + Block::k_codes(t, quarter * (D / 64) + 2 * i));
+      kc[i] = __builtin_nontemporal_load(reinterpret_cast<const KPiece*>(block + Block::k_codes(t, quarter * (D / 64) + 2 * i)));
     ks = *reinterpret_cast<const KScales*>(block + Block::k_scale(t, quarter * (D / 64)));
 #pragma unroll
     for (int i = 0; i < kVScales; ++i) vs[i] = block[Block::v_scale(t, quarter * kVScales + i)];
@@ -508,7 +512,7 @@ __global__ __launch_bounds__(kThreads) void copy_kept(const kv4_cache c, const k
 #pragma unroll
   for (int i = 0; i < kVPieces; ++i) {
     const int j = i * (kThreads / 16) + threadIdx.x / 16;
-    if (from[j]) vc[i] = *reinterpret_cast<const VPiece*>(from[j] + Block::v_codes(token[j], 0) + column * 16);
+    if (from[j]) vc[i] = __builtin_nontemporal_load(reinterpret_cast<const VPiece*>(from[j] + Block::v_codes(token[j], 0) + column * 16));
   }
 #pragma unroll
   for (int i = 0; i < kKPieces; ++i)
