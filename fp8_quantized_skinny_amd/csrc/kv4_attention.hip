@@ -113,7 +113,11 @@ struct Queries {
   }
 };
 
-// A lane's part of a block: K and V codes and scales.
+// A lane's part of a block: K and V codes and scales.  All are loaded
+// non-temporally: a layer's cache is not read again before the rest of the model
+// has passed through the caches.  With the scales alone loaded in the ordinary way
+// 290 MB from cold caches take 67 us instead of 52, with the keys too 89; where
+// all of it stays in the last-level cache between calls, ordinary loads gain 1 or 2%.
 template <int D>
 struct KRegs {
   u32x4 codes[D / 32];
@@ -123,13 +127,13 @@ struct KRegs {
     for (int i = 0; i < D / 32; ++i) codes[i] = load16(block + i * 1024 + lane * 16);
     const uint8_t* s = block + KvBlock<D>::kKScales + lane * (D / 16);
     if constexpr (D == 64) {
-      scales[0] = *reinterpret_cast<const uint32_t*>(s);
+      scales[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(s));
     } else if constexpr (D == 128) {
-      const u32x2 v = *reinterpret_cast<const u32x2*>(s);
+      const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(s));
       scales[0] = v.x;
       scales[1] = v.y;
     } else {
-      const u32x4 v = *reinterpret_cast<const u32x4*>(s);
+      const u32x4 v = load16(s);
 #pragma unroll
       for (int i = 0; i < 4; ++i) scales[i] = v[i];
     }
@@ -154,7 +158,7 @@ struct VRegs {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) codes[i] = load16(block + KvBlock<D>::kVCodes + i * 1024 + lane * 16);
     const int g = lane >> 4, c = lane & 15;
-    const u32x4 v = *reinterpret_cast<const u32x4*>(block + KvBlock<D>::kVScales + (c * (D / 16) / 16) * 64 + g * 16);
+    const u32x4 v = load16(block + KvBlock<D>::kVScales + (c * (D / 16) / 16) * 64 + g * 16);
 #pragma unroll
     for (int i = 0; i < 4; ++i) scales[i] = v[i];
   }
@@ -312,12 +316,12 @@ __device__ __forceinline__ Page page_of(const kv4_cache& c, int id, int page, in
 
 // Workgroups per CU that a wavefront's registers allow.  More was slower where
 // it could be had: four instead of three with one tile at D = 128, for which
-// the keys arrive late, 71 against 67 us (16 sequences of 30000 .. 32768 tokens,
-// 12 rows a head); two instead of one with two tiles at D = 256, 27 against 26.
+// the keys arrive late, 6% more time (16 sequences of 30000 .. 32768
+// tokens, 12 rows a head); two instead of one with two tiles at D = 256, 27 against 26.
 constexpr int attend_per_cu(int D, int MT) { return D == 256 && MT == 2 ? 1 : (D / 64 * MT <= 2 ? 3 : 2); }
 
 // What bounds it: with one tile of queries, memory (16 sequences of 30000 ..
-// 32768 tokens, four heads of 128: 290 MB in 67 us, 4.3 TB/s, where a large copy
+// 32768 tokens, four heads of 128: 290 MB in 52 us, 5.5 TB/s, where a large copy
 // moves 4.7); with three, memory and the widening and softmax about equally
 // (eight sequences of 120000 .. 131072 tokens: 578 MB and 99 GFLOP in 148 us; the
 // VALU is busy for 57% of the cycles and the matrix unit for 28%); short
