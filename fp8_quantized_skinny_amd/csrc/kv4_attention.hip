@@ -49,6 +49,13 @@ struct AttendArgs {
   float scale;
 };
 
+// A row's log-sum, of its reference maximum (log2) and its sum: -inf for a row
+// without weight, and NaN for one with a NaN among its scores.  Maxima pass over
+// NaN, so that a row of nothing else keeps the -inf that it began with; the sum tells.
+__device__ __forceinline__ float log_sum(float m, float total) {
+  return m == -INFINITY && total == 0.0f ? -INFINITY : (m - kLift + __builtin_amdgcn_logf(total)) * kLn2;
+}
+
 // As sum_over_rows, for the greatest.
 __device__ __forceinline__ float max_over_rows(float v) {
   const uint32_t u = __float_as_uint(v);
@@ -546,8 +553,7 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
         uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at_row * D + at * DB);
 #pragma unroll
         for (int d = 0; d < DB; d += 2) dst[d / 2] = elem_pack<E>(x[d], x[d + 1]);
-        if (at == 0 && a.lse)
-          a.lse[at_row] = mm == -INFINITY ? -INFINITY : (mm - kLift + __builtin_amdgcn_logf(total)) * kLn2;
+        if (at == 0 && a.lse) a.lse[at_row] = log_sum(mm, total);
       }
     }
   }
@@ -573,9 +579,12 @@ __global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a) {
   const auto row = [&](int s) { return (static_cast<size_t>(split.x) + static_cast<size_t>(s) * stride) * (MT * 16) + local; };
   float mm = -INFINITY, total = 0.0f;
   f32x4 x{0.0f, 0.0f, 0.0f, 0.0f};
-  const auto add = [&](float m, float l, f32x4 v) {  // a part's reference maximum, sum and values
-    if (m == -INFINITY) return;
-    const float to = fmaxf(mm, m), f0 = __builtin_amdgcn_exp2f(mm - to), f = __builtin_amdgcn_exp2f(m - to);
+  // A part's reference maximum, sum and values.  One without weight has zeros, and
+  // one with nothing but NaN scores the same maximum, -inf, but a NaN sum and values:
+  // both are added, times 0.
+  const auto add = [&](float m, float l, f32x4 v) {
+    const float to = fmaxf(mm, m), about = to == -INFINITY ? 0.0f : to;
+    const float f0 = __builtin_amdgcn_exp2f(mm - about), f = __builtin_amdgcn_exp2f(m - about);
     mm = to;
     total = total * f0 + f * l;
     x = x * f0 + f * v;
@@ -603,8 +612,7 @@ __global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a) {
   x *= mm == -INFINITY ? 0.0f : a.c.gv / total;
   *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at_row * D + at * 4) =
       u32x2{elem_pack<E>(x[0], x[1]), elem_pack<E>(x[2], x[3])};
-  if (at == 0 && a.lse)
-    a.lse[at_row] = mm == -INFINITY ? -INFINITY : (mm - kLift + __builtin_amdgcn_logf(total)) * kLn2;
+  if (at == 0 && a.lse) a.lse[at_row] = log_sum(mm, total);
 }
 
 // ---- weights ----------------------------------------------------------------

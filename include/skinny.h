@@ -555,7 +555,10 @@ int kv4_read(const kv4_cache* cache, void* k, void* v, int type, int n,
  * fp16, relative to the row's greatest.  bf16 queries are scaled to fp16's
  * range by a power of two per row, which changes no value above 2^-39 of the
  * row's greatest.  A NaN among the values of a slot that only some rows see
- * makes those rows NaN and no others. */
+ * makes those rows NaN and no others.  A NaN among the scores of a row (of its
+ * query, or of the key of a slot that it sees) makes its out and lse NaN.  A row
+ * whose scores are all -inf, which takes an infinite query, has no weight
+ * anywhere: its out is zero and its lse -inf. */
 int kv4_attention(const kv4_cache* cache, const kv4_rows* q, int type, int T,
                   int Hq, float scale, void* out, float* lse, void* workspace,
                   size_t workspace_bytes, hipStream_t stream);
