@@ -672,7 +672,9 @@ __global__ __launch_bounds__(kThreads) void add_weights(const WeightArgs a) {
       for (int e = 0; e < 4; ++e) {
         const int r = qg * MT * 16 + mt * 16 + 4 * g + e;
         limit[mt][e] = r < R ? len - (a.T - 1 - r / a.G) : 0;
-        sub[mt][e] = r < R ? a.lse[(static_cast<size_t>(b) * a.T + r / a.G) * a.Hq + h * a.G + r % a.G] * kLog2e : 0.0f;
+        const float lse = r < R ? a.lse[(static_cast<size_t>(b) * a.T + r / a.G) * a.Hq + h * a.G + r % a.G] : 0.0f;
+        // A row of -inf scores only has no weight, and -inf minus itself is NaN.
+        sub[mt][e] = lse == -INFINITY ? INFINITY : lse * kLog2e;
       }
     __syncthreads();
     float cm[MT][4];

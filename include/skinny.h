@@ -567,7 +567,8 @@ size_t kv4_attention_workspace_bytes(int B, int T, int Hq, int Hk, int D,
 
 /* kv4_attention_weights -- adds the attention weights of a step to the slots:
  * acc_out[b][h][s] = acc[b][h][s] + sum over the rows and query heads of h that
- * see slot s of exp(scale * q . k~_s - lse).  Slots past lens get 0.
+ * see slot s of exp(scale * q . k~_s - lse).  A row whose lse is -inf adds
+ * nothing.  Slots past lens get 0.
  *   q, T, Hq, scale, type : as for kv4_attention;  lse: its output.
  *   acc, acc_out : device fp32 [B][Hk][64 * width], 16-byte aligned; they may
  *          be the same buffer.
