@@ -57,6 +57,34 @@ int check_attend(const kv4_cache* c, const kv4_rows* q, int type, int T, int Hq,
   return std::isfinite(scale) && scale > 0.0f ? SKINNY_OK : SKINNY_EINVAL;
 }
 
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y + b.bytes && y < x + a.bytes;
+}
+
+// Whether an output of an eviction lies on one of its inputs or on another
+// output.  A workgroup writes its head's outputs while others still read the
+// lengths, the weights and the pages.
+bool evict_overlaps(const kv4_cache& c, const float* acc, const kv4_cache& d, const int32_t* kept,
+                    const int32_t* new_lens, const float* new_acc, int keep) {
+  const size_t heads = static_cast<size_t>(c.B) * c.Hk, slot = SKINNY_KV_PAGE * sizeof(float);
+  const auto pages = [](const kv4_cache& k) { return Span{k.data, static_cast<size_t>(k.pages) * k.Hk * 72 * k.D}; };
+  const auto table = [](const kv4_cache& k) { return Span{k.table, static_cast<size_t>(k.B) * k.width * 4}; };
+  const Span in[] = {pages(c), table(c), {c.lens, static_cast<size_t>(c.B) * 4}, {acc, heads * c.width * slot}, table(d)};
+  const Span out[] = {pages(d), {kept, heads * keep * 4}, {new_lens, static_cast<size_t>(c.B) * 4}, {new_acc, heads * d.width * slot}};
+  for (size_t i = 0; i < 4; ++i) {
+    for (const Span& s : in)
+      if (overlap(out[i], s)) return true;
+    for (size_t j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return true;
+  }
+  return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -134,6 +162,7 @@ int kv4_evict(const kv4_cache* cache, const float* acc, const kv4_cache* dst, in
   if (!aligned(acc, 16) || !aligned(kept, 4) || !aligned(new_lens, 4) || !aligned(new_acc, 16)) return SKINNY_EALIGN;
   if (!fits_grid(static_cast<int64_t>(cache->B) * cache->Hk, 1024)) return SKINNY_ESHAPE;
   if (!fits_grid(static_cast<int64_t>(cache->B) * kv4_row_pages(keep) * cache->Hk)) return SKINNY_ESHAPE;
+  if (evict_overlaps(*cache, acc, *dst, kept, new_lens, new_acc, keep)) return SKINNY_EINVAL;
   return launch_status(
       launch_kv4_evict(*cache, acc, *dst, kept, new_lens, new_acc, keep, sinks, recent, stream));
 }

@@ -69,7 +69,9 @@ def kv4_evict(cache, table, lens, acc, dst_cache, dst_table, kept, new_lens, new
     pages of dst_table in dst_cache (the first `sinks` and last `recent` always; ties: the lower slot).
 
     acc: fp32 [B, Hk, 64 * width]; kept: int32 [B, Hk, keep] (slots, -1 past the new length);
-    new_lens: int32 [B]; new_acc: fp32 [B, Hk, 64 * dst width] (weights of the kept slots, then 0)."""
+    new_lens: int32 [B]; new_acc: fp32 [B, Hk, 64 * dst width] (weights of the kept slots, then 0).
+    No output may share memory with an input or another output (new_lens with lens, new_acc with acc,
+    dst_cache with cache); cache and dst_cache may be separate ranges of pages of one tensor."""
     _status(native().kv4_evict(cache, table, lens, acc, dst_cache, dst_table, kept, new_lens, new_acc, sinks, recent, stream),
             "kv4_evict")
 

@@ -591,7 +591,11 @@ int kv4_attention_weights(const kv4_cache* cache, const kv4_rows* q, int type,
  *   kept      : device int32 [B][Hk][keep]: the slots kept, -1 past them.
  *   new_lens  : device int32 [B]: min(lens, keep).
  *   new_acc   : device fp32 [B][Hk][64 * dst->width]: their weights, 0 past them.
- *   1 <= keep;  0 <= sinks, recent;  sinks + recent <= keep. */
+ *   1 <= keep;  0 <= sinks, recent;  sinks + recent <= keep.
+ * No output may overlap an input or another output: such a call (new_lens that
+ * is lens, new_acc that is acc, pages of dst among cache's) is refused with
+ * SKINNY_EINVAL.  Separate ranges of pages of one allocation serve as cache and
+ * dst. */
 int kv4_evict(const kv4_cache* cache, const float* acc, const kv4_cache* dst,
               int32_t* kept, int32_t* new_lens, float* new_acc, int keep,
               int sinks, int recent, hipStream_t stream);
