@@ -45,6 +45,10 @@ int check_heads(int T, int Hq, int Hk) {
   return SKINNY_OK;
 }
 
+// The plan of an attention call counts the pages of all sequences, and shares
+// of a page at least, one per sequence, in an int.
+bool fits_plan(int B, int width) { return static_cast<int64_t>(B) * (width + 1) <= INT32_MAX; }
+
 int check_attend(const kv4_cache* c, const kv4_rows* q, int type, int T, int Hq, float scale) {
   int s = check_cache(c, true);
   if (s) return s;
@@ -117,7 +121,7 @@ int kv4_read(const kv4_cache* cache, void* k, void* v, int type, int n, hipStrea
 }
 
 size_t kv4_attention_workspace_bytes(int B, int T, int Hq, int Hk, int D, int width) {
-  if (check_shape(B, Hk, D, width) || check_heads(T, Hq, Hk)) return 0;
+  if (check_shape(B, Hk, D, width) || check_heads(T, Hq, Hk) || !fits_plan(B, width)) return 0;
   return kv4_attend_plan(B, T, Hq, Hk, D, width).total;
 }
 
@@ -127,6 +131,7 @@ int kv4_attention(const kv4_cache* cache, const kv4_rows* q, int type, int T, in
   if (s) return s;
   if (!out) return SKINNY_EINVAL;
   if (!aligned(out, 16) || !aligned(lse, 4)) return SKINNY_EALIGN;
+  if (!fits_plan(cache->B, cache->width)) return SKINNY_ESHAPE;
   const AttendPlan plan = kv4_attend_plan(cache->B, T, Hq, cache->Hk, cache->D, cache->width);
   if (!fits_grid(plan.grid) || !fits_grid(static_cast<int64_t>(cache->B) * cache->Hk * plan.QG)) return SKINNY_ESHAPE;
   const size_t need = plan.total;

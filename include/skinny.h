@@ -492,7 +492,8 @@ int skinny_read_probe_pattern(const void* buf, size_t bytes, int pattern,
  *            1 <= Hk <= 1024;  64 * width < 2^31.
  *   gk, gv : finite and > 0.
  * A call whose sequences, heads and pages make more workgroups than a grid
- * holds (2^24, and B * Hk < 2^22 for kv4_evict) is refused: SKINNY_ESHAPE.
+ * holds (2^24, and B * Hk < 2^22 for kv4_evict) is refused: SKINNY_ESHAPE.  So
+ * is kv4_attention with B * (width + 1) >= 2^31.
  *
  * A table entry outside 0 .. pages - 1 that a sequence's slots reach names no
  * page: nothing is read or written there, its slots are held by nobody
