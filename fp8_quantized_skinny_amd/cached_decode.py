@@ -5,7 +5,9 @@
 A step takes M = streams * rows activations through
     qkv GEMM -> kv4_append -> kv4_attention -> kv4_attention_weights -> o_proj GEMM
     -> lm_head GEMM -> lm_head_logprobs
-with the GEMMs on NVFP4 weights, and continues every stream with its most probable token.  A cache
+with the GEMMs on NVFP4 weights, and continues every stream with its most probable token.  With more
+than one row a step also takes the rows - 1 tokens that follow it, given from outside (a template or a
+grammar forces them; random here), so that no token of a stream goes into the cache twice.  A cache
 that a step would fill past its budget is cut first (kv4_evict) to the slots with the most
 accumulated weight, into a second pool of pages; the two pools take turns.
 
@@ -40,7 +42,9 @@ class CachedDecoder:
         g = torch.Generator(device="cuda")
         g.manual_seed(seed)
         self.embedding = (torch.randn((vocab, hidden), generator=g, device="cuda") * 0.5).half()
+        # The tokens that follow the last step's rows; the last of each stream is not in the cache yet.
         self.tokens = torch.randint(0, vocab, (streams, rows), generator=g, device="cuda", dtype=torch.int32)
+        self.generator = g
 
         width = -(-budget // PAGE)
         pages = torch.randperm(streams * width, generator=g, device="cuda").to(torch.int32).reshape(streams, width)
@@ -81,7 +85,11 @@ class CachedDecoder:
         cut = self.length + T > self.budget
         if cut:
             self.evict()
-        x = self.embedding[self.tokens.flatten().long()]
+        fed = self.tokens[:, -1:]
+        if T > 1:
+            forced = torch.randint(0, self.vocab, (B, T - 1), generator=self.generator, device="cuda", dtype=torch.int32)
+            fed = torch.cat((fed, forced), 1)
+        x = self.embedding[fed.flatten().long()]
         nvfp4_gemm(self.w_qkv, x, self.qkv, workspace=ws)
         heads = self.qkv.view(B, T, Hq + 2 * Hk, D)
         q, k, v = heads[:, :, :Hq], heads[:, :, Hq:Hq + Hk], heads[:, :, Hq + Hk:]
@@ -93,12 +101,12 @@ class CachedDecoder:
         kv4_attention_weights(q, *self.cache(), self.lse, acc, acc)
         nvfp4_gemm(self.w_o, self.out.view(B * T, Hq * D), self.y, workspace=ws)
         nvfp4_gemm(self.w_head, x + self.y, self.logits, workspace=ws)
-        # The log probability of the token that each row is given next: for the rows before a
-        # stream's last that is the following row's; the last is continued greedily.
+        # The log probability of the token that follows each row: for the rows before a
+        # stream's last that is the next row's; the last is continued greedily.
         best = self.logits.view(B, T, -1)[:, -1].argmax(-1).to(torch.int32)
-        given = torch.cat((self.tokens[:, 1:], best[:, None]), 1)
-        lm_head_logprobs(self.logits, given.flatten(), self.logprob, self.entropy, self.top_ids, self.top_logprobs, workspace=ws)
-        self.tokens = given
+        following = torch.cat((fed[:, 1:], best[:, None]), 1)
+        lm_head_logprobs(self.logits, following.flatten(), self.logprob, self.entropy, self.top_ids, self.top_logprobs, workspace=ws)
+        self.tokens = following
         return cut
 
 
