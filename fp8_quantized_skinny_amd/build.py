@@ -1,5 +1,6 @@
 """Build libskinny.so in-tree with hipcc for gfx950, and _binding.so, the Python
-extension that checks torch tensors for some of its calls, with the host compiler.
+extension that checks torch tensors for some of its calls, against the torch in use.
+Where torch cannot be imported the library alone is built.
 
     python -m fp8_quantized_skinny_amd.build
 
@@ -39,8 +40,12 @@ def hipcc():
 
 
 def build(verbose=False):
-    """Build libskinny.so and _binding.so; returns the library path."""
+    """Build libskinny.so and, if torch can be imported, _binding.so; returns the library path."""
     build_library(verbose)
+    try:
+        import torch  # noqa: F401
+    except ImportError:  # host-only use (packing, quantizing): nothing calls the binding
+        return LIB
     build_binding(verbose)
     return LIB
 
@@ -78,7 +83,8 @@ def build_binding(verbose=False):
     include = [INCLUDE, os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
                os.path.join(rocm, "include"), sysconfig.get_paths()["include"]]
     tmp = BINDING + ".tmp"
-    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+    _run([hipcc(), "-no-hip-rt", "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+          "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
           *[f"-I{i}" if i == INCLUDE else f"-isystem{i}" for i in include], os.path.join(CSRC, "binding.cpp"), "-o", tmp,
           "-L" + PKG, "-l:libskinny.so", "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(home, "lib"),
           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"], verbose)
