@@ -97,7 +97,13 @@ def native():
         lib()
         if not os.path.exists(_build.BINDING):
             _build.build_binding()
+        import torch
+
         from . import _binding
+        built = getattr(_binding, "torch_version", "another version")
+        if built != torch.__version__:  # it reads tensors' fields in place
+            raise ImportError(f"{_build.BINDING} was built for torch {built}, this is {torch.__version__}: "
+                              "build again (python -m fp8_quantized_skinny_amd.build)")
         _NATIVE = _binding
     return _NATIVE
 

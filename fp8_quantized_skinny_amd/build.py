@@ -84,7 +84,7 @@ def build_binding(verbose=False):
                os.path.join(rocm, "include"), sysconfig.get_paths()["include"]]
     tmp = BINDING + ".tmp"
     _run([hipcc(), "-no-hip-rt", "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
-          "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+          "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", f'-DSKINNY_TORCH_VERSION="{torch.__version__}"',
           *[f"-I{i}" if i == INCLUDE else f"-isystem{i}" for i in include], os.path.join(CSRC, "binding.cpp"), "-o", tmp,
           "-L" + PKG, "-l:libskinny.so", "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(home, "lib"),
           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"], verbose)
