@@ -40,22 +40,7 @@ struct KvBlock {
   }
 };
 
-// The eight code bytes of token t's group f, from or to a block in global
-// memory or LDS.
-template <int D>
-__device__ __forceinline__ u32x2 kv_codes_load(const uint8_t* block, int t, int f, bool v) {
-  if (!v) return *reinterpret_cast<const u32x2*>(block + KvBlock<D>::k_codes(t, f));
-  const uint8_t* p = block + KvBlock<D>::v_codes(t, f);
-  if constexpr (D == 256) {
-    return *reinterpret_cast<const u32x2*>(p);
-  } else if constexpr (D == 128) {
-    return u32x2{*reinterpret_cast<const uint32_t*>(p), *reinterpret_cast<const uint32_t*>(p + 16)};
-  } else {
-    const auto h = [&](int i) { return static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p + 16 * i)); };
-    return u32x2{h(0) | (h(1) << 16), h(2) | (h(3) << 16)};
-  }
-}
-
+// The eight code bytes of token t's group f, to a block in global memory or LDS.
 template <int D>
 __device__ __forceinline__ void kv_codes_store(uint8_t* block, int t, int f, bool v, u32x2 c) {
   if (!v) {
@@ -76,7 +61,7 @@ __device__ __forceinline__ void kv_codes_store(uint8_t* block, int t, int f, boo
   }
 }
 
-// Half of those: positions 8 piece .. 8 piece + 7.
+// Half of a group's, from a block: positions 8 piece .. 8 piece + 7.
 template <int D>
 __device__ __forceinline__ uint32_t kv_codes_load_half(const uint8_t* block, int t, int piece, bool v) {
   const int f = piece / 2, half = piece % 2;

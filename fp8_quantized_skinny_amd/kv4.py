@@ -23,7 +23,8 @@ def _status(status, where):
 
 
 def _buffer(t, dtype, shape, name, device):
-    """The address of a contiguous device tensor of exactly this type and shape, as every call below checks it."""
+    """The address of a contiguous device tensor of exactly this type and shape.  The calls below make this check in
+    the extension module itself; here it can be reached without a GPU, for tests of its refusals."""
     return native().buffer(t, dtype, tuple(shape), name, device)
 
 
