@@ -69,7 +69,10 @@ __device__ __forceinline__ float max_over_rows(float v) {
 // A workgroup's query rows: loaded before its keys, since loads arrive in
 // order, then put into LDS as fp16 with a row stride of D + 8 halves (16 bytes
 // off the banks' period).  bf16 rows are scaled by the power of two that brings
-// their greatest value to 2^14 .. 2^15; `factor` undoes it.
+// their greatest value to 2^14 .. 2^15; `factor` undoes it.  A bf16 value has
+// eight bits and fp16's least step is 2^-24: what is scaled to 2^-17 or more,
+// 2^-31 of the greatest, keeps them all, and the rest is off by 2^-39 of the
+// greatest at most.
 template <int D, int MT>
 struct Queries {
   static constexpr int kPer = D / 8;  // threads per row
@@ -330,8 +333,8 @@ constexpr int attend_per_cu(int D, int MT) { return D == 256 && MT == 2 ? 1 : (D
 // What bounds it: with one tile of queries, memory (16 sequences of 30000 ..
 // 32768 tokens, four heads of 128: 290 MB in 52 us, 5.5 TB/s, where a large copy
 // moves 4.7); with three, memory and the widening and softmax about equally
-// (eight sequences of 120000 .. 131072 tokens: 578 MB and 99 GFLOP in 148 us; the
-// VALU is busy for 57% of the cycles and the matrix unit for 28%); short
+// (eight sequences of 120000 .. 131072 tokens: 578 MB and 99 GFLOP in 145 us; the
+// VALU is busy for 59% of the cycles and the matrix unit for 29%); short
 // sequences, latency: of one sequence of 8197 tokens' 16 us a page takes 2.6
 // and the joining of four wavefronts' sums 3.
 template <int D, int MT, class E>
@@ -621,8 +624,9 @@ __global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a) {
 // rows is a sum of its own values and of four lanes.
 // The log-sum is known only when a row's last share is done, so the keys are
 // read twice; keeping the scores instead would move 48 bytes a token and head
-// each way for 12 rows, the keys are 72.  Bound by memory: 16 sequences of 30000
-// .. 32768 tokens, four heads of 128, 161 MB in 36 us (4.5 TB/s).
+// each way for 12 rows, the keys are 72.  With few rows a head (up to 0.07 D) the
+// scores would be the smaller; that form is not built.  Bound by memory: 16
+// sequences of 30000 .. 32768 tokens, four heads of 128, 161 MB in 32 us (5 TB/s).
 struct WeightArgs {
   kv4_cache c;
   kv4_rows q;
@@ -764,9 +768,14 @@ hipError_t by_shape(int D, int type, int tiles, M most, F f) {
 // Four times what the CUs hold in place of the latter: 128 sequences of 1 ..
 // 8000 tokens, four heads of 128, one row, 89 us against 71, of 8000 each 135
 // against 108, with four rows 134 against 117; seven batches of a few long and
-// many short sequences took from 2% less to 52% more.  A share has a page per wavefront at least, two
-// where one tile of queries makes a page cheaper than joining another share;
-// a table of no more pages needs no join.
+// many short sequences took from 2% less to 52% more.
+//
+// A share has a page per wavefront at least, and with one tile of queries two, so
+// that up to 512 tokens need no join (301 tokens: 6.7 us in one launch; 600, which
+// do: 10 to 11).  Longer sequences lose and gain about as much.  Two pages against
+// one, one tile, four heads of 128: one sequence of 8197 tokens 12.1 us against
+// 11.1, four of 8000 .. 9000 14.3 against 14.9, 32 of up to 20000 44.1 against 44.3;
+// three tiles: 8197 tokens 18.8 against 19.2, 2000 tokens 17.0 against 16.1.
 AttendPlan kv4_attend_plan(int B, int T, int Hq, int Hk, int D, int width) {
   AttendPlan p;
   constexpr int kCUs = 256;
@@ -814,6 +823,10 @@ hipError_t launch_kv4_weights(const kv4_cache& c, const kv4_rows& q, int type, i
                               const float* lse, const float* acc, float* acc_out, hipStream_t stream) {
   const int G = Hq / c.Hk, all = (T * G + 15) / 16, tiles = all < kWeightTiles ? all : kWeightTiles;
   const int64_t pages = static_cast<int64_t>(c.B) * c.Hk * c.width;
+  // Pages of a workgroup: one per wavefront, and up to four where there are
+  // enough for 1024 workgroups, which pays for the queries once.  One: 42.6 us,
+  // two: 36.0, four: 33.2, eight: 32.2 (16 sequences of 30000 .. 32768 tokens, four
+  // heads of 128, one row); 9.8, 12.7, 18.5 and 29.8 (one of 8197, eight rows).
   int64_t per = pages / 1024;
   per = per < kWaves ? kWaves : (per > 16 ? 16 : per);
   WeightArgs a{c, q, lse, acc, acc_out, T, Hq, G, static_cast<int>(per), scale};

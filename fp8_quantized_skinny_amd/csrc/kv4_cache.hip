@@ -182,7 +182,9 @@ __global__ __launch_bounds__(kThreads) void append(const kv4_cache c, const kv4_
   if (whole) store_image<D>(block, image);
 }
 
-// Eight held values from their codes and scale, rounded once to E.
+// Eight held values from their codes and scale.  code * scale is exact; the product
+// with g is rounded to fp32 and then to E, so a result next to the middle of two
+// of E's values can be the farther one (by 2^-24 of itself).
 template <class E>
 __device__ __forceinline__ u32x4 held8(uint32_t codes, uint32_t scale, float g) {
   const float s = e4m3f<0>(scale);
@@ -466,7 +468,7 @@ __global__ __launch_bounds__(kSelectThreads) void select_slots(const kv4_cache c
 // the source are loaded non-temporally: they are done with, and what is written
 // here is read next.  Bound by memory: keeping a third of the slots touches
 // nearly every line of the source, so 16 sequences x 4 heads x 8192 slots kept
-// of 20000 .. 32768 read 232 MB and write 75 MB, in 58 us (94 with the caches'
+// of 20000 .. 32768 read 232 MB and write 75 MB, in 58 to 61 us (94 with the caches'
 // own order; 64, and 10 more for the reading that follows, with the stores
 // non-temporal too).
 template <int D>

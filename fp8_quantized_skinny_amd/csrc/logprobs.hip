@@ -15,11 +15,11 @@
 // has something to add); the groups that are left at the end are read again.
 //
 // Bound by the VALU where there are many rows (12 operations an element, seven
-// of them for the sums): 2048 rows of 151936 bf16 logits, 20 alternatives,
-// take 116 us, 5.4 TB/s.  Collecting every element above the threshold took
-// 240 us; 131 with loads behind a branch, each waited for at once.  Eight such
-// rows of fp16 take 11 us, which is latency: a load, two cuts, and the meeting
-// of 38 workgroups per row.
+// of them for the sums): 2048 rows of 151936 bf16 logits, 20 alternatives, take
+// 115 to 120 us pass after pass, 5.2 to 5.4 TB/s, and 121 from cold caches.
+// Collecting every element above the threshold took 240 us; 131 with loads behind
+// a branch, each waited for at once.  Eight such rows of fp16 take 11 us, which is
+// latency: a load, two cuts, and the meeting of 38 workgroups per row.
 #include <hip/hip_runtime.h>
 
 #include "kv4.cuh"
@@ -436,8 +436,11 @@ __global__ __launch_bounds__(kThreads) void logprobs(const LogprobArgs a) {
   finish<L>(a, r, x, st, groups, merge_lists(lists, counts, a.k, groups, &number));
 }
 
-// Workgroups per row: enough of them to fill the chip, each with one step of
-// its wavefronts at least.
+// Workgroups per row: 2048 of all rows, eight per CU, each with one step of its
+// wavefronts at least.  Up to 32 rows of 151936 logits the step decides; beyond,
+// each workgroup's fixed part (its cuts, its meeting with the others) shows: 128
+// rows, 20 alternatives, fp16 / fp32: 24 / 29 us, with 1024 workgroups 21 / 25, 512
+// 22 / 26, 256 25 / 34, 4096 37 / 37; 512 rows 44 / 60, 42 / 58, 42 / 58, 42 / 58 and 53 / 67.
 int row_splits(int R, int V) {
   constexpr int kStep = kThreads * kMost;
   const int want = 2048 / R, most = (V + kStep - 1) / kStep;

@@ -60,7 +60,7 @@ def kv4_attention_weights(q, cache, table, lens, lse, acc, acc_out, scale=None, 
     """acc_out = acc + the attention weights of the step's rows, per key/value head and slot.
 
     q, cache, table, lens, scale, gk: as given to kv4_attention; lse: its output (fp32 [B, T, Hq]);
-    acc, acc_out: fp32 [B, Hk, 64 * width], possibly the same tensor."""
+    acc, acc_out: fp32 [B, Hk, 64 * width], the same tensor or two that do not overlap."""
     _status(native().kv4_attention_weights(q, cache, table, lens, lse, acc, acc_out, scale, gk, stream), "kv4_attention_weights")
     return acc_out
 
@@ -86,6 +86,7 @@ def lm_head_logprobs(logits, tokens, logprob, entropy, top_ids, top_logprobs, wo
     """Log probabilities of tokens (int32 [R]) under logits (fp16, bf16 or fp32 [R, V], rows contiguous),
     the rows' entropies, and their k greatest logits' indices and log probabilities (ties: the lower index).
 
+    logits begin at a multiple of 16 bytes (their rows need not).
     logprob, entropy: fp32 [R]; top_ids: int32 [R, k]; top_logprobs: fp32 [R, k], k = 1..32.
     workspace: from new_workspace(lm_head_logprobs_workspace_bytes(R, V, k)) when that is > 0."""
     _status(native().lm_head_logprobs(logits, tokens, logprob, entropy, top_ids, top_logprobs, workspace, stream),

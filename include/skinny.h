@@ -537,7 +537,8 @@ int kv4_append(const kv4_cache* cache, const kv4_rows* k, const kv4_rows* v,
                int type, int T, hipStream_t stream);
 
 /* kv4_read -- the newest n slots as held: k and v, device [B][n][Hk][D] of
- * `type`, row t = slot lens - n + t, zeros where that is negative. */
+ * `type`, row t = slot lens - n + t, zeros where that is negative.  Values are
+ * rounded to fp32 and then to `type`. */
 int kv4_read(const kv4_cache* cache, void* k, void* v, int type, int n,
              hipStream_t stream);
 
@@ -554,8 +555,9 @@ int kv4_read(const kv4_cache* cache, void* k, void* v, int type, int n,
  *          (see "Workspaces").
  * Scores, the softmax and the sums are fp32; the weights of V~ are rounded to
  * fp16, relative to the row's greatest.  bf16 queries are scaled to fp16's
- * range by a power of two per row, which changes no value above 2^-39 of the
- * row's greatest.  A NaN among the values of a slot that only some rows see
+ * range by a power of two per row: values down to 2^-31 of the row's greatest
+ * (or of 2^-100, if that is more) are exact, and smaller ones are off by 2^-39 of
+ * it at most.  A NaN among the values of a slot that only some rows see
  * makes those rows NaN and no others.  A NaN among the scores of a row (of its
  * query, or of the key of a slot that it sees) makes its out and lse NaN.  A row
  * whose scores are all -inf, which takes an infinite query, has no weight
@@ -571,8 +573,8 @@ size_t kv4_attention_workspace_bytes(int B, int T, int Hq, int Hk, int D,
  * see slot s of exp(scale * q . k~_s - lse).  A row whose lse is -inf adds
  * nothing.  Slots past lens get 0.
  *   q, T, Hq, scale, type : as for kv4_attention;  lse: its output.
- *   acc, acc_out : device fp32 [B][Hk][64 * width], 16-byte aligned; they may
- *          be the same buffer.
+ *   acc, acc_out : device fp32 [B][Hk][64 * width], 16-byte aligned: the same
+ *          buffer, or two that do not overlap.
  * gv and the values are not used. */
 int kv4_attention_weights(const kv4_cache* cache, const kv4_rows* q, int type,
                           int T, int Hq, float scale, const float* lse,
