@@ -414,4 +414,6 @@ def layers_run(layers, xs, ys, workspace=None, stream=None):
 
 
 from .kv4 import (kv4_append, kv4_read, kv4_attention, kv4_attention_workspace_bytes, kv4_attention_weights,  # noqa: E402
-                  kv4_evict, lm_head_logprobs, lm_head_logprobs_workspace_bytes)
+                  kv4_evict, lm_head_logprobs, lm_head_logprobs_workspace_bytes, kv4_attention_window,
+                  kv4_attention_window_workspace_bytes, kv4_attention_chunk, kv4_attention_chunk_workspace_bytes,
+                  qk_norm_rope, rope_inv_freq)

@@ -55,6 +55,12 @@ def _declare(lib):
         "kv4_read": (c_int, [P, P, P, c_int, c_int, P]),
         "kv4_attention": (c_int, [P, P, c_int, c_int, c_int, c_float, P, P, P, c_size_t, P]),
         "kv4_attention_workspace_bytes": (c_size_t, [c_int] * 6),
+        "kv4_attention_window": (c_int, [P, P, c_int, c_int, c_int, c_float, c_int, c_int, P, P, P, c_size_t, P]),
+        "kv4_attention_window_workspace_bytes": (c_size_t, [c_int] * 8),
+        "kv4_attention_chunk": (c_int, [P, P, ctypes.c_int64, ctypes.c_int64, P, c_int, c_int, c_int, c_float, c_int, c_int,
+                                        P, P, P, c_size_t, P]),
+        "kv4_attention_chunk_workspace_bytes": (c_size_t, [c_int] * 8),
+        "qk_norm_rope": (c_int, [P, P, P, P, P, P, *[c_int] * 8, c_float, c_float, P, P, P]),
         "kv4_attention_weights": (c_int, [P, P, c_int, c_int, c_int, c_float, P, P, P, P]),
         "kv4_evict": (c_int, [P, P, P, P, P, P, c_int, c_int, c_int, P]),
         "lm_head_logprobs": (c_int, [P, c_int, ctypes.c_int64, P, P, P, P, P, c_int, c_int, c_int, P, c_size_t, P]),
@@ -117,4 +123,5 @@ EXPORTED = ("nvfp4_pack", "nvfp4_gemm", "fp8_gemm", "lm_head_gemm_argmax", "nvfp
             "fp8_gemm_packed_config", "skinny_default_config", "nvfp4_gemm_noalloc",
             "skinny_read_probe_pattern", "kv4_append", "kv4_read", "kv4_attention",
             "kv4_attention_workspace_bytes", "kv4_attention_weights", "kv4_evict", "lm_head_logprobs",
-            "lm_head_logprobs_workspace_bytes")
+            "lm_head_logprobs_workspace_bytes", "kv4_attention_window", "kv4_attention_window_workspace_bytes",
+            "kv4_attention_chunk", "kv4_attention_chunk_workspace_bytes", "qk_norm_rope")

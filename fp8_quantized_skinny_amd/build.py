@@ -25,7 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libskinny.so")
 BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["host.cpp", "nvfp4_gemm.hip", "fp8_gemm.hip", "reduce.hip", "probe.hip", "noalloc.hip",
-           "kv4_host.cpp", "kv4_cache.hip", "kv4_attention.hip", "logprobs.hip"]
+           "kv4_host.cpp", "kv4_cache.hip", "kv4_attention.hip", "kv4_chunk.hip", "rope.hip", "logprobs.hip"]
 ARCH = "gfx950"
 
 # Kernels known to spill, with their scratch bytes per lane: the streaming

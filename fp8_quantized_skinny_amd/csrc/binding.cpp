@@ -1,5 +1,5 @@
 // Python entry of the calls whose buffers are checked as torch tensors: the
-// 4-bit key/value cache and the log probabilities.  Ten attributes of each of
+// 4-bit key/value cache, the norm and rotation before it and the log probabilities.  Ten attributes of each of
 // six tensors, read from Python, took longer than the kernels of a small call
 // (append and read of eight rows: 23 us a pass then, 10 this way); here they
 // are fields.  Every function returns the status of the C call it makes.
@@ -203,6 +203,79 @@ int attention(PyObject* const* a, int dev) {  // q, cache, table, lens, out, lse
   return kv4_attention(&c, &q.rows, type_of(q.type), T, Hq, scale, out, lse, ws.data, ws.bytes, stream_of(a[10], dev));
 }
 
+// q, cache, table, lens, out, window, sinks, lse, scale, gk, gv, workspace, stream
+int attention_window(PyObject* const* a, int dev) {
+  const kv4_cache c = cache_of(a[1], a[2], a[3], number(a[9]), number(a[10]), dev);
+  const Rows q = queries(a[0], c, dev);
+  const int T = as_int(q.shape[1], "T"), Hq = as_int(q.shape[2], "Hq"), window = integer(a[5]), sinks = integer(a[6]);
+  void* out = buffer(a[4], q.type, q.shape, "out", dev);
+  float* lse = a[7] == Py_None ? nullptr : floats(a[7], {c.B, T, Hq}, "lse", dev);
+  const float scale = a[8] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(c.D))) : number(a[8]);
+  const Scratch ws = scratch(a[11], kv4_attention_window_workspace_bytes(c.B, T, Hq, c.Hk, c.D, c.width, window, sinks),
+                             "kv4_attention_window", dev);
+  return kv4_attention_window(&c, &q.rows, type_of(q.type), T, Hq, scale, window, sinks, out, lse, ws.data, ws.bytes,
+                              stream_of(a[12], dev));
+}
+
+// q, starts, cache, table, lens, out, lse, scale, window, sinks, gk, gv, workspace, stream
+int attention_chunk(PyObject* const* a, int dev) {
+  const kv4_cache c = cache_of(a[2], a[3], a[4], number(a[10]), number(a[11]), dev);
+  const at::Tensor& q = tensor(a[0], "q");
+  on_device(q, "q", dev);
+  if (type_of(q.scalar_type()) < 0 || q.dim() != 3) type_error("q must be float16 or bfloat16 [N, Hq, D]");
+  const auto n = q.sizes(), s = q.strides();
+  if (n[0] < 1 || n[1] < 1) value_error("q is empty");
+  if (n[2] != c.D) value_error("q must be [N, Hq, D] with D = " + std::to_string(c.D) + ", got " + list(n));
+  if (s[2] != 1) value_error("the last dimension of q must be contiguous");
+  const int N = as_int(n[0], "N"), Hq = as_int(n[1], "Hq"), window = integer(a[8]), sinks = integer(a[9]);
+  const int32_t* starts = ints(a[1], {c.B + 1}, "starts", dev);
+  void* out = buffer(a[5], q.scalar_type(), n, "out", dev);
+  float* lse = a[6] == Py_None ? nullptr : floats(a[6], {N, Hq}, "lse", dev);
+  const float scale = a[7] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(c.D))) : number(a[7]);
+  const Scratch ws = scratch(a[12], kv4_attention_chunk_workspace_bytes(N, c.B, Hq, c.Hk, c.D, c.width, window, sinks),
+                             "kv4_attention_chunk", dev);
+  return kv4_attention_chunk(&c, q.data_ptr(), N > 1 ? s[0] : 0, Hq > 1 ? s[1] : 0, starts, N, type_of(q.scalar_type()), Hq,
+                             scale, window, sinks, out, lse, ws.data, ws.bytes, stream_of(a[13], dev));
+}
+
+// q, k, positions, inv_freq, q_out, k_out, q_weight, k_weight, eps, amplitude, interleaved, stream
+int norm_rope(PyObject* const* a, int dev) {
+  // [N, heads, D] is one sequence of N tokens.
+  const auto heads = [&](PyObject* o, const std::string& name) {
+    const at::Tensor& t = tensor(o, name);
+    on_device(t, name, dev);
+    const auto type = type_of(t.scalar_type());
+    const int64_t d = t.dim();
+    if ((type != SKINNY_F16 && type != SKINNY_BF16) || (d != 3 && d != 4))
+      type_error(name + " must be float16 or bfloat16 [B, T, heads, D] or [N, heads, D]");
+    const auto n = t.sizes(), s = t.strides();
+    for (const int64_t x : n)
+      if (x < 1) value_error(name + " is empty");
+    if (s[d - 1] != 1 && n[d - 1] > 1) value_error("the last dimension of " + name + " must be contiguous");
+    return Rows{{t.data_ptr(), d == 4 && n[0] > 1 ? s[0] : 0, n[d - 3] > 1 ? s[d - 3] : 0, n[d - 2] > 1 ? s[d - 2] : 0}, n, t.scalar_type()};
+  };
+  const Rows q = heads(a[0], "q"), k = heads(a[1], "k"), qo = heads(a[4], "q_out"), ko = heads(a[5], "k_out");
+  const size_t d = q.shape.size();
+  const int64_t D = q.shape[d - 1];
+  if (k.shape.size() != d || k.shape[d - 1] != D || k.shape.slice(0, d - 2) != q.shape.slice(0, d - 2))
+    value_error("k must have q's tokens and head size " + list(q.shape) + ", got " + list(k.shape));
+  if (qo.shape != q.shape) value_error("q_out must be " + list(q.shape) + ", got " + list(qo.shape));
+  if (ko.shape != k.shape) value_error("k_out must be " + list(k.shape) + ", got " + list(ko.shape));
+  if (k.type != q.type || qo.type != q.type || ko.type != q.type) type_error("q, k, q_out and k_out must have one type");
+  const int32_t* positions = ints(a[2], q.shape.slice(0, d - 2), "positions", dev);
+  const at::Tensor& f = tensor(a[3], "inv_freq");
+  if (f.dim() != 1) value_error("inv_freq must be float32 [rot / 2]");
+  const float* freq = floats(a[3], f.sizes(), "inv_freq", dev);
+  const int rot = 2 * as_int(f.size(0) < (1 << 20) ? f.size(0) : 1 << 20, "rot");
+  const float* qw = a[6] == Py_None ? nullptr : floats(a[6], {D}, "q_weight", dev);
+  const float* kw = a[7] == Py_None ? nullptr : floats(a[7], {D}, "k_weight", dev);
+  const int interleaved = PyObject_IsTrue(a[10]);
+  if (interleaved < 0) throw PythonError{};
+  return qk_norm_rope(&q.rows, &k.rows, positions, rot ? freq : nullptr, qw, kw, type_of(q.type), as_int(d == 4 ? q.shape[0] : 1, "B"),
+                      as_int(q.shape[d - 3], "T"), as_int(q.shape[d - 2], "Hq"), as_int(k.shape[d - 2], "Hk"), as_int(D, "D"), rot,
+                      interleaved, number(a[8]), number(a[9]), &qo.rows, &ko.rows, stream_of(a[11], dev));
+}
+
 int weights(PyObject* const* a, int dev) {  // q, cache, table, lens, lse, acc, acc_out, scale, gk, stream
   const kv4_cache c = cache_of(a[1], a[2], a[3], number(a[8]), 1.0f, dev);
   const Rows q = queries(a[0], c, dev);
@@ -285,6 +358,9 @@ PyMethodDef method(const char* name, F* f) {
 PyMethodDef methods[] = {method("kv4_append", entry<append, 8>),
                          method("kv4_read", entry<read, 8>),
                          method("kv4_attention", entry<attention, 11>),
+                         method("kv4_attention_window", entry<attention_window, 13>),
+                         method("kv4_attention_chunk", entry<attention_chunk, 14>),
+                         method("qk_norm_rope", entry<norm_rope, 12>),
                          method("kv4_attention_weights", entry<weights, 10>),
                          method("kv4_evict", entry<evict, 12>),
                          method("lm_head_logprobs", entry<logprobs, 8>),

@@ -47,7 +47,32 @@ struct AttendArgs {
   int T, Hq, G, QG;
   int least;     // fewest pages of a share
   float scale;
+  int window, sinks;  // windowed calls: a row with limit L sees the slots from L - window on, and those below sinks
 };
+
+// The pages that a sequence's rows see: all up to its length, or with a window
+// the first `low`, which hold the sinks, and those from `from` on, where the
+// earliest row's window begins.
+template <bool WINDOW>
+struct View {
+  int low, from, end;
+  __device__ __forceinline__ View(const AttendArgs& a, int len) : low(0), from(0), end((len + kPage - 1) / kPage) {
+    if constexpr (WINDOW) {
+      const int least = len - (a.T - 1) - a.window;
+      from = least > 0 ? least / kPage : 0;
+      low = a.sinks / kPage + (a.sinks % kPage != 0);
+      low = low < from ? low : from;
+    }
+  }
+  __device__ __forceinline__ int pages() const { return WINDOW ? low + end - from : end; }
+  __device__ __forceinline__ int page(int v) const { return !WINDOW || v < low ? v : v - low + from; }
+};
+
+// Whether a row with this limit does not see the slot.
+template <bool WINDOW>
+__device__ __forceinline__ bool hidden(const AttendArgs& a, int slot, int limit) {
+  return slot >= limit || (WINDOW && slot < limit - a.window && slot >= a.sinks);
+}
 
 // A row's log-sum, of its reference maximum (log2) and its sum: -inf for a row
 // without weight, and NaN for one with a NaN among its scores.  Maxima pass over
@@ -205,9 +230,9 @@ __device__ __forceinline__ f16x2 e2m1_pos(u32x2 pair, int s) {  // position s (0
 // that the codes stand for 0 and not for NaN.  A NaN in a slot that only later
 // rows see must not reach the others through a weight of 0: such scales become
 // 0 too, and the rows that do see the slot are made NaN by hand.
-template <int D, int MT>
-__device__ __forceinline__ void clean_values(VRegs<D>& v, int first, int len, int lane, const int (&limit)[MT],
-                                             f32x4 (&o)[MT][D / 16]) {
+template <bool WINDOW, int D, int MT>
+__device__ __forceinline__ void clean_values(const AttendArgs& a, VRegs<D>& v, int first, int len, int lane,
+                                             const int (&limit)[MT], f32x4 (&o)[MT][D / 16]) {
   const int g = lane >> 4;
   uint32_t bad = 0u;
 #pragma unroll
@@ -230,7 +255,7 @@ __device__ __forceinline__ void clean_values(VRegs<D>& v, int first, int len, in
     bool seen = false;
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      seen |= ((bad >> i) & 1u) && first + 16 * (i / 4) + 4 * g + i % 4 < limit[mt];
+      seen |= ((bad >> i) & 1u) && !hidden<WINDOW>(a, first + 16 * (i / 4) + 4 * g + i % 4, limit[mt]);
     // Lanes of one query hold different positions: all four rows of lanes.
     if (max_over_rows(seen ? 1.0f : 0.0f) > 0.0f) {
 #pragma unroll
@@ -249,7 +274,11 @@ struct Share {
   int b, h, qg, len, p0, p1, splits, first;  // first: the segment's first share; the next is Hk * QG further
   bool any;
 };
-__device__ __forceinline__ Share plan_share(const kv4_cache& c, int QG, int least, int lane) {
+template <bool WINDOW>
+__device__ __forceinline__ Share plan_share(const AttendArgs& a, int lane) {
+  const kv4_cache& c = a.c;
+  const int QG = a.QG, least = a.least;
+  const auto seen = [&](int len) { return View<WINDOW>(a, len).pages(); };
   const int per = c.Hk * QG;                      // segments of a sequence
   const int room = static_cast<int>(gridDim.x) / per;  // shares per head and query group; at least B
   const int at = static_cast<int>(blockIdx.x) / per;
@@ -263,14 +292,14 @@ __device__ __forceinline__ Share plan_share(const kv4_cache& c, int QG, int leas
     s.any = true;
     s.b = at;
     s.len = kv_len_uniform(c, at);
-    s.p1 = (s.len + kPage - 1) / kPage;
+    s.p1 = seen(s.len);
     s.splits = 1;
     s.first = static_cast<int>(blockIdx.x);
     return s;
   }
-  const auto pages = [&](int b) { return b < c.B ? (kv_len(c, b) + kPage - 1) / kPage : 0; };
+  const auto pages = [&](int b) { return b < c.B ? seen(kv_len(c, b)) : 0; };
   const int held = lane < c.B ? kv_len(c, lane) : 0;  // of the first 64 sequences
-  int mine = (held + kPage - 1) / kPage, total = 0;
+  int mine = seen(held), total = 0;
   for (int b0 = 0; b0 < c.B; b0 += 64)
     total += __builtin_amdgcn_readlane(wave_scan(b0 ? pages(b0 + lane) : mine), 63);
   int chunk = total / (room - (c.B >> 1)) + 1;
@@ -297,7 +326,7 @@ __device__ __forceinline__ Share plan_share(const kv4_cache& c, int QG, int leas
       const int first = __builtin_amdgcn_readlane(upto, l) - s.splits;
       s.first = first * per + hq;
       s.len = b0 ? kv_len_uniform(c, s.b) : __builtin_amdgcn_readlane(held, l);
-      const int np = (s.len + kPage - 1) / kPage, each = (np + s.splits - 1) / s.splits;
+      const int np = seen(s.len), each = (np + s.splits - 1) / s.splits;
       s.p0 = (at - first) * each;
       s.p1 = s.p0 + each < np ? s.p0 + each : np;
       break;
@@ -337,7 +366,7 @@ constexpr int attend_per_cu(int D, int MT) { return D == 256 && MT == 2 ? 1 : (D
 // VALU is busy for 59% of the cycles and the matrix unit for 29%); short
 // sequences, latency: of one sequence of 8197 tokens' 16 us a page takes 2.6
 // and the joining of four wavefronts' sums 3.
-template <int D, int MT, class E>
+template <int D, int MT, class E, bool WINDOW>
 __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const AttendArgs a) {
   constexpr int DB = D / 16;
   constexpr int kRow = D + 8;
@@ -349,14 +378,15 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
   __shared__ float stat[kWaves][MT * 16][2];
   __shared__ __align__(16) float sums[kWaves][D * 16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, c = lane & 15;
-  const Share sh = plan_share(a.c, a.QG, a.least, lane);
+  const Share sh = plan_share<WINDOW>(a, lane);
   if (!sh.any) return;
   const int b = sh.b, h = sh.h, qg = sh.qg, len = sh.len;
   const int R = a.T * a.G;
   if (a.split && sh.first == static_cast<int>(blockIdx.x) && threadIdx.x == 0)
     a.split[(b * a.c.Hk + h) * a.QG + qg] = int2{sh.first, sh.splits};
   const int32_t* table = a.c.table + static_cast<size_t>(b) * a.c.width;
-  int page = sh.p0 + wave;
+  const View<WINDOW> view(a, len);
+  int page = sh.p0 + wave;  // of those that the sequence's rows see
   Queries<D, MT> q;
   q.load(a.q, b, h, qg, a.G, R);
   KRegs<D> k;
@@ -364,8 +394,8 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
   Page now{nullptr, 0}, next{nullptr, 0};
   int next_id = 0;
   if (page < sh.p1) {
-    now = page_of<D>(a.c, uniform_load(table, page), page, h);
-    next_id = uniform_load(table, page + kWaves < sh.p1 ? page + kWaves : page);
+    now = page_of<D>(a.c, uniform_load(table, view.page(page)), view.page(page), h);
+    next_id = uniform_load(table, view.page(page + kWaves < sh.p1 ? page + kWaves : page));
     k.load(now.block, lane);
     v.load(now.block, lane);
   }
@@ -393,8 +423,8 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
   for (; page < sh.p1; page += kWaves) {
     const int first = now.first;
     // Past the last page the prefetch reads this one again.
-    next = page + kWaves < sh.p1 ? page_of<D>(a.c, next_id, page + kWaves, h) : now;
-    next_id = uniform_load(table, page + 2 * kWaves < sh.p1 ? page + 2 * kWaves : page);
+    next = page + kWaves < sh.p1 ? page_of<D>(a.c, next_id, view.page(page + kWaves), h) : now;
+    next_id = uniform_load(table, view.page(page + 2 * kWaves < sh.p1 ? page + 2 * kWaves : page));
     f32x4 s[4][MT];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -417,7 +447,8 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (!kLateKeys) k.load(next.block, lane);
-    if (first > len - (a.T - 1) - kPage) {  // some row does not see the whole page
+    // Some row does not see the whole page.
+    if (first > len - (a.T - 1) - kPage || (WINDOW && first < len - a.window && first + kPage > a.sinks)) {
       int limit[MT];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) limit[mt] = limits[mt * 16 + c];
@@ -427,8 +458,8 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (first + 16 * j + 4 * g + e >= limit[mt]) s[j][mt][e] = -INFINITY;
-      clean_values<D, MT>(v, first, len, lane, limit, o);
+            if (hidden<WINDOW>(a, first + 16 * j + 4 * g + e, limit[mt])) s[j][mt][e] = -INFINITY;
+      clean_values<WINDOW, D, MT>(a, v, first, len, lane, limit, o);
     }
     bool grow = false;
     float top[MT];
@@ -776,8 +807,15 @@ hipError_t by_shape(int D, int type, int tiles, M most, F f) {
 // one, one tile, four heads of 128: one sequence of 8197 tokens 12.1 us against
 // 11.1, four of 8000 .. 9000 14.3 against 14.9, 32 of up to 20000 44.1 against 44.3;
 // three tiles: 8197 tokens 18.8 against 19.2, 2000 tokens 17.0 against 16.1.
-AttendPlan kv4_attend_plan(int B, int T, int Hq, int Hk, int D, int width) {
+//
+// With a window a sequence's rows see at most the pages of window + T - 1 slots in
+// a row and those of the sinks, and the plan goes by these instead of the width.
+AttendPlan kv4_attend_plan(int B, int T, int Hq, int Hk, int D, int width, int window, int sinks) {
   AttendPlan p;
+  if (window) {
+    const int64_t pages = (static_cast<int64_t>(window) + T + 61) / kPage + 1 + (static_cast<int64_t>(sinks) + kPage - 1) / kPage;
+    width = pages < width ? static_cast<int>(pages) : width;
+  }
   constexpr int kCUs = 256;
   const int tiles = (T * (Hq / Hk) + 15) / 16;
   p.QG = (tiles + max_tiles(D) - 1) / max_tiles(D);
@@ -801,11 +839,11 @@ AttendPlan kv4_attend_plan(int B, int T, int Hq, int Hk, int D, int width) {
   return p;
 }
 
-hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type, int T, int Hq, float scale, void* out,
-                                float* lse, void* workspace, hipStream_t stream) {
-  const AttendPlan p = kv4_attend_plan(c.B, T, Hq, c.Hk, c.D, c.width);
+hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type, int T, int Hq, float scale, int window,
+                                int sinks, void* out, float* lse, void* workspace, hipStream_t stream) {
+  const AttendPlan p = kv4_attend_plan(c.B, T, Hq, c.Hk, c.D, c.width, window, sinks);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  AttendArgs a{c, q, out, lse, nullptr, nullptr, nullptr, T, Hq, Hq / c.Hk, p.QG, p.least, scale};
+  AttendArgs a{c, q, out, lse, nullptr, nullptr, nullptr, T, Hq, Hq / c.Hk, p.QG, p.least, scale, window, sinks};
   if (p.split) {
     a.part = reinterpret_cast<float*>(ws + p.part_off);
     a.stat = reinterpret_cast<float*>(ws + p.stat_off);
@@ -813,7 +851,9 @@ hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type,
   }
   const unsigned segments = static_cast<unsigned>(c.B * c.Hk * p.QG);
   return by_shape(c.D, type, p.MT, [](int D) constexpr { return max_tiles(D); }, [&](auto d, auto mt, auto e) {
-    attend<d(), mt(), decltype(e)><<<dim3(static_cast<unsigned>(p.grid)), kThreads, 0, stream>>>(a);
+    const dim3 grid(static_cast<unsigned>(p.grid));
+    if (window) attend<d(), mt(), decltype(e), true><<<grid, kThreads, 0, stream>>>(a);
+    else attend<d(), mt(), decltype(e), false><<<grid, kThreads, 0, stream>>>(a);
     if (p.split)
       attend_join<d(), mt(), decltype(e)><<<dim3(segments, mt() * 16), kThreads, 0, stream>>>(a);
   });

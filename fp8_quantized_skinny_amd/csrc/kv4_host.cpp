@@ -1,5 +1,6 @@
-// Host side of the 4-bit key/value cache and of the log probabilities:
-// argument checks before any HIP call.
+// Host side of the 4-bit key/value cache, of the norm and rotation before it and
+// of the log probabilities: argument checks before any HIP call.
+#include <algorithm>
 #include <cmath>
 
 #include "kv4_internal.h"
@@ -61,6 +62,13 @@ int check_attend(const kv4_cache* c, const kv4_rows* q, int type, int T, int Hq,
   return std::isfinite(scale) && scale > 0.0f ? SKINNY_OK : SKINNY_EINVAL;
 }
 
+int check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (!need) return SKINNY_OK;
+  if (!workspace) return SKINNY_EINVAL;
+  if (!aligned(workspace, 16)) return SKINNY_EALIGN;
+  return bytes < need ? SKINNY_ESIZE : SKINNY_OK;
+}
+
 struct Span {
   const void* p;
   size_t bytes;
@@ -86,6 +94,97 @@ bool evict_overlaps(const kv4_cache& c, const float* acc, const kv4_cache& d, co
     for (size_t j = 0; j < i; ++j)
       if (overlap(out[i], out[j])) return true;
   }
+  return false;
+}
+
+// A window is given, and one that no table's slots outgrow is none.
+int check_window(int window, int sinks) { return window >= 0 && sinks >= 0 ? SKINNY_OK : SKINNY_EINVAL; }
+int used_window(int window, int width) { return window < static_cast<int64_t>(width) * SKINNY_KV_PAGE ? window : 0; }
+
+int attend(const kv4_cache* cache, const kv4_rows* q, int type, int T, int Hq, float scale, int window, int sinks,
+           void* out, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  int s = check_attend(cache, q, type, T, Hq, scale);
+  if (s) return s;
+  s = check_window(window, sinks);
+  if (s) return s;
+  if (!out) return SKINNY_EINVAL;
+  if (!aligned(out, 16) || !aligned(lse, 4)) return SKINNY_EALIGN;
+  if (!fits_plan(cache->B, cache->width)) return SKINNY_ESHAPE;
+  window = used_window(window, cache->width);
+  const AttendPlan plan = kv4_attend_plan(cache->B, T, Hq, cache->Hk, cache->D, cache->width, window, sinks);
+  if (!fits_grid(plan.grid) || !fits_grid(static_cast<int64_t>(cache->B) * cache->Hk * plan.QG)) return SKINNY_ESHAPE;
+  s = check_workspace(workspace, workspace_bytes, plan.total);
+  if (s) return s;
+  return launch_status(launch_kv4_attention(*cache, *q, type, T, Hq, scale, window, sinks, out, lse, workspace, stream));
+}
+
+int check_chunk(int N, int B, int Hq, int Hk, int D, int width) {
+  const int s = check_shape(B, Hk, D, width);
+  if (s) return s;
+  if (N < 1 || Hq < 1 || Hq % Hk != 0 || Hq / Hk > SKINNY_KV_MAX_GROUP) return SKINNY_ESHAPE;
+  return static_cast<int64_t>(N) * (Hq / Hk) <= INT32_MAX ? SKINNY_OK : SKINNY_ESHAPE;
+}
+bool chunk_fits(const ChunkPlan& p, int Hk) { return p.tiles < (int64_t{1} << 30) && fits_grid(p.shares * Hk, 512); }
+
+// [B][T][H][D] views of 16-bit elements, for qk_norm_rope.
+struct Heads {
+  const kv4_rows* r;
+  int H;
+};
+// The elements from the first of a token's heads to the last.
+int64_t token_extent(const Heads& v, int D) { return (v.H - 1) * (v.H > 1 ? v.r->head : 0) + D; }
+int64_t view_extent(const Heads& v, int B, int T, int D) {
+  return (B > 1 ? (B - 1) * v.r->sequence : 0) + (T > 1 ? (T - 1) * v.r->row : 0) + token_extent(v, D);
+}
+// Whether every head has a place of its own: ordered by stride, each dimension
+// steps over all of those before it.
+bool apart(const Heads& v, int B, int T, int D) {
+  struct Dim {
+    int64_t stride;
+    int count;
+  } d[3] = {{v.r->sequence, B}, {v.r->row, T}, {v.r->head, v.H}};
+  std::sort(d, d + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  int64_t extent = D;
+  for (const Dim& x : d) {
+    if (x.count == 1) continue;
+    if (x.stride < extent) return false;
+    extent += x.stride * (x.count - 1);
+  }
+  return true;
+}
+bool same_heads(const Heads& a, const Heads& b, int B, int T) {
+  return a.r->data == b.r->data && a.H == b.H && (B == 1 || a.r->sequence == b.r->sequence) &&
+         (T == 1 || a.r->row == b.r->row) && (a.H == 1 || a.r->head == b.r->head);
+}
+// Whether two views share no element, as far as that shows: they lie one behind
+// the other, or side by side in sequences or in tokens of the same strides.
+bool disjoint(const Heads& a, const Heads& b, int B, int T, int D) {
+  const int64_t x = reinterpret_cast<intptr_t>(a.r->data), y = reinterpret_cast<intptr_t>(b.r->data);
+  if (x + 2 * view_extent(a, B, T, D) <= y || y + 2 * view_extent(b, B, T, D) <= x) return true;
+  if (x > y) return disjoint(b, a, B, T, D);
+  if (B > 1 && a.r->sequence != b.r->sequence) return false;
+  const int64_t at = (y - x) / 2;
+  if (at >= view_extent(a, 1, T, D) && at + view_extent(b, 1, T, D) <= a.r->sequence) return true;
+  if (T > 1 && a.r->row != b.r->row) return false;
+  int64_t step = INT64_MAX;
+  if (B > 1) step = std::min(step, a.r->sequence);
+  if (T > 1) step = std::min(step, a.r->row);
+  return at >= token_extent(a, D) && at + token_extent(b, D) <= step;
+}
+
+// Whether an output of a chunk call lies on an input or on the other output; out
+// on q itself does not: a workgroup reads the values that it or its join writes.
+bool chunk_overlaps(const kv4_cache& c, const void* q, int64_t row, int64_t head, const int32_t* starts, int N, int Hq,
+                    const void* out, const float* lse, const void* workspace, size_t need) {
+  const size_t values = static_cast<size_t>(N) * Hq * c.D * 2;
+  const Span o{out, values}, l{lse, lse ? static_cast<size_t>(N) * Hq * 4 : 0},
+      x{q, 2 * static_cast<size_t>((N - 1) * row + (Hq - 1) * head + c.D)};
+  const bool same = out == q && (N == 1 || row == static_cast<int64_t>(Hq) * c.D) && (Hq == 1 || head == c.D);
+  const Span in[] = {{c.data, static_cast<size_t>(c.pages) * c.Hk * 72 * c.D}, {c.table, static_cast<size_t>(c.B) * c.width * 4},
+                     {c.lens, static_cast<size_t>(c.B) * 4}, {starts, static_cast<size_t>(c.B + 1) * 4}, {workspace, need}};
+  if ((!same && overlap(o, x)) || (lse && (overlap(l, x) || overlap(l, o)))) return true;
+  for (const Span& s : in)
+    if (overlap(o, s) || (lse && overlap(l, s))) return true;
   return false;
 }
 
@@ -121,26 +220,85 @@ int kv4_read(const kv4_cache* cache, void* k, void* v, int type, int n, hipStrea
 }
 
 size_t kv4_attention_workspace_bytes(int B, int T, int Hq, int Hk, int D, int width) {
-  if (check_shape(B, Hk, D, width) || check_heads(T, Hq, Hk) || !fits_plan(B, width)) return 0;
-  return kv4_attend_plan(B, T, Hq, Hk, D, width).total;
+  return kv4_attention_window_workspace_bytes(B, T, Hq, Hk, D, width, 0, 0);
 }
 
 int kv4_attention(const kv4_cache* cache, const kv4_rows* q, int type, int T, int Hq, float scale, void* out,
                   float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
-  const int s = check_attend(cache, q, type, T, Hq, scale);
+  return attend(cache, q, type, T, Hq, scale, 0, 0, out, lse, workspace, workspace_bytes, stream);
+}
+
+size_t kv4_attention_window_workspace_bytes(int B, int T, int Hq, int Hk, int D, int width, int window, int sinks) {
+  if (check_shape(B, Hk, D, width) || check_heads(T, Hq, Hk) || !fits_plan(B, width) || check_window(window, sinks)) return 0;
+  return kv4_attend_plan(B, T, Hq, Hk, D, width, used_window(window, width), sinks).total;
+}
+
+int kv4_attention_window(const kv4_cache* cache, const kv4_rows* q, int type, int T, int Hq, float scale, int window,
+                         int sinks, void* out, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return attend(cache, q, type, T, Hq, scale, window, sinks, out, lse, workspace, workspace_bytes, stream);
+}
+
+size_t kv4_attention_chunk_workspace_bytes(int N, int B, int Hq, int Hk, int D, int width, int window, int sinks) {
+  if (check_chunk(N, B, Hq, Hk, D, width) || check_window(window, sinks)) return 0;
+  const ChunkPlan p = kv4_chunk_plan(N, B, Hq, Hk, D, width, used_window(window, width), sinks);
+  return chunk_fits(p, Hk) ? p.total : 0;
+}
+
+int kv4_attention_chunk(const kv4_cache* cache, const void* q, int64_t row, int64_t head, const int32_t* starts, int N,
+                        int type, int Hq, float scale, int window, int sinks, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream) {
+  int s = check_cache(cache, true);
   if (s) return s;
-  if (!out) return SKINNY_EINVAL;
-  if (!aligned(out, 16) || !aligned(lse, 4)) return SKINNY_EALIGN;
-  if (!fits_plan(cache->B, cache->width)) return SKINNY_ESHAPE;
-  const AttendPlan plan = kv4_attend_plan(cache->B, T, Hq, cache->Hk, cache->D, cache->width);
-  if (!fits_grid(plan.grid) || !fits_grid(static_cast<int64_t>(cache->B) * cache->Hk * plan.QG)) return SKINNY_ESHAPE;
-  const size_t need = plan.total;
-  if (need) {
-    if (!workspace) return SKINNY_EINVAL;
-    if (!aligned(workspace, 16)) return SKINNY_EALIGN;
-    if (workspace_bytes < need) return SKINNY_ESIZE;
+  s = check_type(type);
+  if (s) return s;
+  s = check_chunk(N, cache->B, Hq, cache->Hk, cache->D, cache->width);
+  if (s) return s;
+  const kv4_rows rows{q, 0, row, head};
+  s = check_rows(&rows);
+  if (s) return s;
+  s = check_window(window, sinks);
+  if (s) return s;
+  if (!starts || !out || !std::isfinite(scale) || scale <= 0.0f) return SKINNY_EINVAL;
+  if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(starts, 4)) return SKINNY_EALIGN;
+  window = used_window(window, cache->width);
+  const ChunkPlan p = kv4_chunk_plan(N, cache->B, Hq, cache->Hk, cache->D, cache->width, window, sinks);
+  if (!chunk_fits(p, cache->Hk)) return SKINNY_ESHAPE;
+  s = check_workspace(workspace, workspace_bytes, p.total);
+  if (s) return s;
+  if (chunk_overlaps(*cache, q, row, head, starts, N, Hq, out, lse, workspace, p.total)) return SKINNY_EINVAL;
+  return launch_status(launch_kv4_chunk(*cache, q, row, head, starts, N, type, Hq, scale, window, sinks, out, lse,
+                                        workspace, stream));
+}
+
+int qk_norm_rope(const kv4_rows* q, const kv4_rows* k, const int32_t* positions, const float* inv_freq,
+                 const float* q_weight, const float* k_weight, int type, int B, int T, int Hq, int Hk, int D, int rot,
+                 int interleaved, float eps, float amplitude, const kv4_rows* q_out, const kv4_rows* k_out,
+                 hipStream_t stream) {
+  int s = check_type(type);
+  if (s) return s;
+  if (D != 64 && D != 128 && D != 256) return SKINNY_ESHAPE;
+  if (B < 1 || T < 1 || Hq < 1 || Hk < 1 || Hq > 65536 || Hk > 65536) return SKINNY_ESHAPE;
+  if (static_cast<int64_t>(B) * T > INT32_MAX || !fits_grid(rope_groups(B * T, Hq, Hk, D))) return SKINNY_ESHAPE;
+  if (rot < 0 || rot > D || rot % 16 != 0) return SKINNY_ESHAPE;
+  for (const kv4_rows* r : {q, k, q_out, k_out}) {
+    s = check_rows(r);
+    if (s) return s;
   }
-  return launch_status(launch_kv4_attention(*cache, *q, type, T, Hq, scale, out, lse, workspace, stream));
+  if (!positions || (rot && !inv_freq) || (interleaved != 0 && interleaved != 1)) return SKINNY_EINVAL;
+  if (!std::isfinite(eps) || eps < 0.0f || !std::isfinite(amplitude)) return SKINNY_EINVAL;
+  if (!aligned(positions, 4) || !aligned(inv_freq, 4) || !aligned(q_weight, 4) || !aligned(k_weight, 4)) return SKINNY_EALIGN;
+  const Heads qi{q, Hq}, ki{k, Hk}, qo{q_out, Hq}, ko{k_out, Hk};
+  if (!apart(qo, B, T, D) || !apart(ko, B, T, D) || !disjoint(qo, ko, B, T, D)) return SKINNY_EINVAL;
+  if (!disjoint(qo, ki, B, T, D) || !disjoint(ko, qi, B, T, D)) return SKINNY_EINVAL;
+  if (!same_heads(qo, qi, B, T) && !disjoint(qo, qi, B, T, D)) return SKINNY_EINVAL;
+  if (!same_heads(ko, ki, B, T) && !disjoint(ko, ki, B, T, D)) return SKINNY_EINVAL;
+  const Span in[] = {{positions, static_cast<size_t>(B) * T * 4}, {inv_freq, static_cast<size_t>(rot) * 2},
+                     {q_weight, q_weight ? D * sizeof(float) : 0}, {k_weight, k_weight ? D * sizeof(float) : 0}};
+  for (const Heads* o : {&qo, &ko})
+    for (const Span& i : in)
+      if (i.bytes && overlap(Span{o->r->data, static_cast<size_t>(view_extent(*o, B, T, D)) * 2}, i)) return SKINNY_EINVAL;
+  const RopeArgs a{*q, *k, *q_out, *k_out, positions, inv_freq, q_weight, k_weight, B * T, T, Hq, Hk, rot, eps, amplitude};
+  return launch_status(launch_norm_rope(a, type, D, interleaved, stream));
 }
 
 int kv4_attention_weights(const kv4_cache* cache, const kv4_rows* q, int type, int T, int Hq, float scale,

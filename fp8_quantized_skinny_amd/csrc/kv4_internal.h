@@ -1,5 +1,5 @@
 // Internal declarations shared by the host code and the kernels of the 4-bit
-// key/value cache and of the log probabilities.  (Apart from internal.h, whose
+// key/value cache, of what stands around it and of the log probabilities.  (Apart from internal.h, whose
 // code the GEMMs' counter measurements are tied to.)
 #ifndef SKINNY_KV4_INTERNAL_H
 #define SKINNY_KV4_INTERNAL_H
@@ -9,8 +9,9 @@
 
 namespace skinny {
 
-// The 4-bit key/value cache and the log probabilities (kv4_cache.hip,
-// kv4_attention.hip, logprobs.hip).  Arguments are validated.
+// The 4-bit key/value cache, the norm and rotation before it and the log
+// probabilities (kv4_cache.hip, kv4_attention.hip, kv4_chunk.hip, rope.hip,
+// logprobs.hip).  Arguments are validated.
 // Pages that `rows` newest slots can reach.
 int kv4_row_pages(int rows);
 hipError_t launch_kv4_append(const kv4_cache& c, const kv4_rows& k, const kv4_rows& v, int type, int T,
@@ -27,11 +28,30 @@ struct AttendPlan {
   int64_t grid;
   size_t split_off, stat_off, part_off, total;
 };
-AttendPlan kv4_attend_plan(int B, int T, int Hq, int Hk, int D, int width);
-hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type, int T, int Hq, float scale, void* out,
-                                float* lse, void* workspace, hipStream_t stream);
+AttendPlan kv4_attend_plan(int B, int T, int Hq, int Hk, int D, int width, int window, int sinks);  // window 0: none
+hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type, int T, int Hq, float scale, int window,
+                                int sinks, void* out, float* lse, void* workspace, hipStream_t stream);
 hipError_t launch_kv4_weights(const kv4_cache& c, const kv4_rows& q, int type, int T, int Hq, float scale,
                               const float* lse, const float* acc, float* acc_out, hipStream_t stream);
+// How a chunk call is laid out: the most tiles of rows, tiles that are split, parts
+// of them and shares, each per key/value head, and the workspace.
+struct ChunkPlan {
+  int64_t tiles, splits, parts, shares;
+  size_t counts_off, begin_off, offset_off, share_off, split_off, stat_off, part_off, total;
+};
+ChunkPlan kv4_chunk_plan(int N, int B, int Hq, int Hk, int D, int width, int window, int sinks);
+hipError_t launch_kv4_chunk(const kv4_cache& c, const void* q, int64_t row, int64_t head, const int32_t* starts, int N,
+                            int type, int Hq, float scale, int window, int sinks, void* out, float* lse, void* workspace,
+                            hipStream_t stream);
+struct RopeArgs {
+  kv4_rows q, k, q_out, k_out;
+  const int32_t* positions;
+  const float *inv_freq, *q_weight, *k_weight;
+  int tokens, T, Hq, Hk, rot;
+  float eps, amplitude;
+};
+int64_t rope_groups(int tokens, int Hq, int Hk, int D);  // workgroups of a call, at most
+hipError_t launch_norm_rope(const RopeArgs& a, int type, int D, bool interleaved, hipStream_t stream);
 size_t logprobs_workspace(int R, int V, int k);
 hipError_t launch_logprobs(const void* logits, int type, int64_t stride, const int32_t* tokens, float* logprob,
                            float* entropy, int32_t* top_ids, float* top_logprobs, int R, int V, int k,

@@ -1,4 +1,4 @@
-"""The 4-bit key/value cache and the lm_head's log probabilities: Python binding.
+"""The 4-bit key/value cache, the norm and rotation before it and the lm_head's log probabilities: Python binding.
 
 The functions have the names of the C ABI in include/skinny.h, which documents
 layouts and values; here device buffers are torch tensors and their sizes are
@@ -9,6 +9,8 @@ stream: a torch stream, a raw handle, or None for torch's current stream.
     table  int32 [B, width]              the pages of each sequence
     lens   int32 [B]                     slots of each sequence, the step's own tokens among them
 """
+
+import numpy as np
 
 from ._lib import lib, native
 
@@ -54,6 +56,70 @@ def kv4_attention(q, cache, table, lens, out, lse=None, scale=None, gk=1.0, gv=1
     workspace: from new_workspace(kv4_attention_workspace_bytes(...))."""
     _status(native().kv4_attention(q, cache, table, lens, out, lse, scale, gk, gv, workspace, stream), "kv4_attention")
     return out
+
+
+def kv4_attention_window_workspace_bytes(B, T, Hq, Hk, D, width, window, sinks=0):
+    """Workspace bytes of kv4_attention_window (0: none needed, or an unsupported shape)."""
+    return lib().kv4_attention_window_workspace_bytes(B, T, Hq, Hk, D, width, window, sinks)
+
+
+def kv4_attention_window(q, cache, table, lens, out, window, sinks=0, lse=None, scale=None, gk=1.0, gv=1.0, workspace=None, stream=None):
+    """kv4_attention within a sliding window: of its slots s < L (L = lens - (T - 1 - t)) a row sees those with
+    s >= L - window and the first `sinks` of the sequence.  window 0: all of them.
+
+    workspace: from new_workspace(kv4_attention_window_workspace_bytes(...)); the rest as kv4_attention."""
+    _status(native().kv4_attention_window(q, cache, table, lens, out, window, sinks, lse, scale, gk, gv, workspace, stream),
+            "kv4_attention_window")
+    return out
+
+
+def kv4_attention_chunk_workspace_bytes(N, B, Hq, Hk, D, width, window=0, sinks=0):
+    """Workspace bytes of kv4_attention_chunk (0: an unsupported shape)."""
+    return lib().kv4_attention_chunk_workspace_bytes(N, B, Hq, Hk, D, width, window, sinks)
+
+
+def kv4_attention_chunk(q, starts, cache, table, lens, out, lse=None, scale=None, window=0, sinks=0, gk=1.0, gv=1.0, workspace=None,
+                        stream=None):
+    """Attention of chunks of new tokens, which the cache holds already: rows starts[b] .. starts[b + 1] - 1 of q are
+    sequence b's newest tokens, each over the slots up to its own (with a window, as kv4_attention_window).
+
+    q: fp16 or bf16 [N, Hq, D], views allowed; starts: int32 [B + 1]; out: q's shape and type, contiguous;
+    lse: fp32 [N, Hq] or None.  Rows that no sequence has are left as they were.
+    workspace: from new_workspace(kv4_attention_chunk_workspace_bytes(...)) with the same window and sinks."""
+    _status(native().kv4_attention_chunk(q, starts, cache, table, lens, out, lse, scale, window, sinks, gk, gv, workspace, stream),
+            "kv4_attention_chunk")
+    return out
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_weight=None, k_weight=None, eps=1e-6, amplitude=1.0, interleaved=False,
+                 stream=None):
+    """The norm of each query and key head (over its D values, times a weight; none without weights) and the rotation of
+    its first 2 * len(inv_freq) positions by the angles positions * inv_freq, in one pass.
+
+    q, k: fp16 or bf16 [B, T, heads, D] or [N, heads, D], views allowed; positions: int32 [B, T] or [N]; inv_freq: fp32
+    [rot / 2], radians per position (see rope_inv_freq); weights: fp32 [D] or None; q_out, k_out: as q and k, or q and k
+    themselves; amplitude: a factor of the rotated positions.  Pairs are (i, i + rot / 2), interleaved (2 i, 2 i + 1)."""
+    _status(native().qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_weight, k_weight, eps, amplitude, interleaved, stream),
+            "qk_norm_rope")
+    return q_out, k_out
+
+
+def rope_inv_freq(rot, base=10000.0, factor=1.0, original=0, fast=32.0, slow=1.0):
+    """The frequencies of qk_norm_rope, float32 [rot / 2] (host): base ** (-2 i / rot), for contexts `factor` times those
+    that a model was trained on divided by factor.  With `original`, the positions it was trained on, only the pairs that turn
+    fewer than `slow` times over these are divided by all of it, those of more than `fast` turns stay, and between
+    them the share falls in a straight line over the pairs' indices (YaRN: Peng et al., 2023, whose amplitude is 0.1 ln(factor) + 1)."""
+    if rot < 0 or rot % 2 or base <= 1.0 or factor <= 0.0 or original < 0 or not fast > slow > 0.0:
+        raise ValueError("rot must be even, base > 1, factor > 0, original >= 0 and fast > slow > 0")
+    i = np.arange(rot // 2, dtype=np.float64)
+    freq = base ** (-2.0 * i / max(rot, 1))
+    stay = np.zeros_like(freq)
+    if original:
+        # The index at which a pair makes n turns over the original positions.
+        at = lambda n: rot * np.log(original / (n * 2.0 * np.pi)) / (2.0 * np.log(base))  # noqa: E731
+        low, high = max(np.floor(at(fast)), 0.0), min(np.ceil(at(slow)), rot - 1.0)
+        stay = 1.0 - np.clip((i - low) / max(high - low, 1e-3), 0.0, 1.0)
+    return (freq * stay + freq / factor * (1.0 - stay)).astype(np.float32)
 
 
 def kv4_attention_weights(q, cache, table, lens, lse, acc, acc_out, scale=None, gk=1.0, stream=None):

@@ -568,6 +568,53 @@ int kv4_attention(const kv4_cache* cache, const kv4_rows* q, int type, int T,
 size_t kv4_attention_workspace_bytes(int B, int T, int Hq, int Hk, int D,
                                      int width);
 
+/* kv4_attention_window -- kv4_attention of rows that see a sliding window and the
+ * sequence's first tokens: of the slots below its limit L = lens - (T - 1 - t) a
+ * row sees those from L - window on, its own among them, and those below
+ * `sinks`.  window 0: all of them, as kv4_attention.  Pages that no row of the
+ * step sees are not read, and what they hold reaches no result.
+ *   window, sinks : >= 0.
+ *   workspace : kv4_attention_window_workspace_bytes(...) bytes, which with a
+ *          window goes by the pages that can be seen, and by width only where
+ *          that is less.
+ * Everything else as kv4_attention. */
+int kv4_attention_window(const kv4_cache* cache, const kv4_rows* q, int type,
+                         int T, int Hq, float scale, int window, int sinks,
+                         void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream);
+size_t kv4_attention_window_workspace_bytes(int B, int T, int Hq, int Hk, int D,
+                                            int width, int window, int sinks);
+
+/* kv4_attention_chunk -- attention of chunks of new tokens, of any length and
+ * another for each sequence, over the cache that already holds them.
+ *   q    : device [N][Hq][D] of `type`, rows `row` and heads `head` elements
+ *          apart (as in kv4_rows); the sequences' rows one after another.
+ *   starts : device, int32 [B + 1]: the rows of sequence b are starts[b] ..
+ *          starts[b + 1] - 1, any number from none on.  A start outside 0 .. N
+ *          counts as the nearer of these and one below an earlier start as that
+ *          one, so that no row has two sequences.
+ *   Row i of a sequence's n stands for slot lens - n + i.  It sees the slots
+ *   below L = lens - (n - 1 - i) that kv4_attention_window's window and sinks
+ *   leave it (window 0: all of them).
+ *   out  : device [N][Hq][D] of `type`, contiguous; zeros for a row that sees no
+ *          slot.
+ *   lse  : device fp32 [N][Hq] or NULL: -inf for a row that sees no slot.
+ *   workspace : kv4_attention_chunk_workspace_bytes(...) bytes (see "Workspaces";
+ *          never NULL).
+ *   1 <= N, N * (Hq / Hk) < 2^31; Hq as for kv4_attention.
+ * Rows before starts[0] and from starts[B] on are left as they were, in out and in
+ * lse.  out may be q itself (the same pointer and strides); otherwise neither out
+ * nor lse may share memory with an input, the workspace or the other:
+ * SKINNY_EINVAL.  Scores, softmax, roundings, bad pages and NaN are as for
+ * kv4_attention. */
+int kv4_attention_chunk(const kv4_cache* cache, const void* q, int64_t row,
+                        int64_t head, const int32_t* starts, int N, int type,
+                        int Hq, float scale, int window, int sinks, void* out,
+                        float* lse, void* workspace, size_t workspace_bytes,
+                        hipStream_t stream);
+size_t kv4_attention_chunk_workspace_bytes(int N, int B, int Hq, int Hk, int D,
+                                           int width, int window, int sinks);
+
 /* kv4_attention_weights -- adds the attention weights of a step to the slots:
  * acc_out[b][h][s] = acc[b][h][s] + sum over the rows and query heads of h that
  * see slot s of exp(scale * q . k~_s - lse).  A row whose lse is -inf adds
@@ -602,6 +649,39 @@ int kv4_attention_weights(const kv4_cache* cache, const kv4_rows* q, int type,
 int kv4_evict(const kv4_cache* cache, const float* acc, const kv4_cache* dst,
               int32_t* kept, int32_t* new_lens, float* new_acc, int keep,
               int sinks, int recent, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * qk_norm_rope -- the norm of each query and key head and the rotation of its
+ * position, between the qkv GEMM and kv4_append (RMSNorm: Zhang and Sennrich,
+ * "Root Mean Square Layer Normalization", 2019; rotary positions: Su et al.,
+ * "RoFormer", 2021).  For a head x of D values at position p:
+ *   u = x * weight / sqrt(mean(x^2) + eps), or u = x where the weight is NULL;
+ *   c_i, s_i = amplitude * cos, sin(p * inv_freq[i]),  i = 0 .. rot/2 - 1;
+ *   interleaved = 0: y[i] = u[i] c_i - u[i + rot/2] s_i,
+ *                    y[i + rot/2] = u[i + rot/2] c_i + u[i] s_i;
+ *   interleaved = 1: the same of the pairs u[2i] and u[2i + 1];
+ *   y[d] = u[d] for d >= rot.
+ * All of it in fp32 and the angles in fp64 (right to 2^-24 of a turn at every
+ * position, for frequencies up to 1), and y rounded once.  A scaling of the positions for long contexts is
+ * in inv_freq, and one of the result (YaRN's) in amplitude.
+ *   q, k, q_out, k_out : [B][T][Hq or Hk][D] of `type` by strides, as kv4_rows.
+ *          q_out may be q, and k_out k: the same pointer and strides.  Otherwise
+ *          no output may share memory with an input or with the other output
+ *          (views side by side in the tokens or sequences of one buffer serve):
+ *          SKINNY_EINVAL.
+ *   positions : device, int32 [B][T], any values.
+ *   inv_freq  : device, fp32 [rot/2], radians per position (NULL if rot is 0).
+ *   q_weight, k_weight : device, fp32 [D], each may be NULL.
+ *   D 64, 128 or 256;  rot a multiple of 16, 0 .. D;  1 <= Hq, Hk <= 65536;
+ *   eps >= 0;  B * T < 2^31 and at most 2^24 workgroups (one has up to four times
+ *   512 / D heads of a token): SKINNY_ESHAPE.
+ * ------------------------------------------------------------------------- */
+int qk_norm_rope(const kv4_rows* q, const kv4_rows* k, const int32_t* positions,
+                 const float* inv_freq, const float* q_weight,
+                 const float* k_weight, int type, int B, int T, int Hq, int Hk,
+                 int D, int rot, int interleaved, float eps, float amplitude,
+                 const kv4_rows* q_out, const kv4_rows* k_out,
+                 hipStream_t stream);
 
 /* ---------------------------------------------------------------------------
  * lm_head_logprobs -- log probabilities from an lm_head's logits, one pass.

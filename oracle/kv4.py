@@ -1,4 +1,4 @@
-"""The 4-bit key/value cache and the log probabilities, written as their definitions in float64.
+"""The 4-bit key/value cache, what stands around it and the log probabilities, written as their definitions in float64.
 
 ORACLE -- test infrastructure only; shares no code with the library.
 
@@ -86,6 +86,28 @@ def kv_attend(q, k, v, held, limit, scale):
     e = np.exp(x - m)
     p[see] = e / e.sum()
     return p[see] @ v[see], m + np.log(e.sum()), p, p[see] @ np.abs(v[see])
+
+
+def in_window(n, limit, window, sinks):
+    """Which of n slots a row with this limit sees (window 0: all below the limit)."""
+    s = np.arange(n)
+    return (s < limit) & ((s >= limit - window) | (s < sinks) if window else True)
+
+
+def norm_rope(x, weight, eps, position, inv_freq, amplitude, interleaved):
+    """One head x [D] at a position: y [D], and what bounds its rounding: |u| of both positions of a pair."""
+    u = np.asarray(x, np.float64)
+    if weight is not None:
+        u = u * np.asarray(weight, np.float64) / np.sqrt((u * u).mean() + float(np.float32(eps)))
+    y, size = u.copy(), np.abs(u)
+    half = len(inv_freq)
+    for i in range(half):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+        angle = float(position) * float(inv_freq[i])
+        c, s = float(np.float32(amplitude)) * np.cos(angle), float(np.float32(amplitude)) * np.sin(angle)
+        y[a], y[b] = u[a] * c - u[b] * s, u[b] * c + u[a] * s
+        size[a] = size[b] = abs(float(np.float32(amplitude))) * (abs(u[a]) + abs(u[b]))
+    return y, size
 
 
 def kv_evict(acc, n, keep, sinks, recent):
