@@ -222,12 +222,12 @@ __device__ __forceinline__ float sum_over_halves(float v) {
 // fp16 of a page: keys by token, values by position (position c * D/16 + j in row 16 j + c).
 // Rows are 16 bytes off the banks' period, so that 16 lanes' pieces of 16 neighbouring rows meet all banks.
 template <int D>
-struct Tile {
+struct alignas(16) Tile {
   static constexpr int kKeyRow = D + 8, kValueRow = kPage + 8;
   _Float16 k[kPage * kKeyRow];
   _Float16 v[D * kValueRow];
-  uint32_t bad[kPage];  // groups of 16 positions of a token that are NaN and were made 0
-  uint32_t any;
+  uint32_t bad[kPage];  // groups of 16 positions of a token that are NaN and were made 0,
+  uint32_t any[4];      // where a tile of 16 tokens has one
 };
 
 // A thread's part of a page: of tile p of 16 tokens, lane l of the first four
@@ -337,18 +337,73 @@ __device__ __forceinline__ void widen_values(const Raw<D>& r, uint32_t scale, Ti
   }
 }
 
-// Of a page that some row does not see whole, NaN values become 0 and are noted:
-// a weight of 0 must not carry them to the rows that do not see them.
+// Of a page that some row does not see whole, or that is none, NaN values become 0
+// and are noted: a weight of 0 must not carry them to the rows that do not see them.
 template <int D>
 __device__ __forceinline__ uint32_t note_bad(uint32_t scale, Tile<D>* to, int p, int lane) {
+  const uint32_t wrong = ((scale & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  const bool any = __any(wrong != 0u);
+  to->any[p] = any;
+  if (any) {
+    if (lane < 16) to->bad[16 * p + lane] = 0u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (((scale >> (8 * i)) & 0x7Fu) == 0x7Fu) {
-      scale &= ~(0xFFu << (8 * i));
-      atomicOr(&to->bad[16 * p + 4 * (lane >> 4) + i], 1u << ((lane & 15) * D / 256));
-      to->any = 1u;
-    }
+    for (int i = 0; i < 4; ++i)
+      if ((wrong >> (8 * i + 7)) & 1u) {
+        scale &= ~(0xFFu << (8 * i));
+        atomicOr(&to->bad[16 * p + 4 * (lane >> 4) + i], 1u << ((lane & 15) * D / 256));
+      }
+  }
   return scale;
+}
+
+// A barrier for what went to LDS; loads of the next page stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+}
+
+// A wavefront's rows, or its part of them where the tile is split.
+template <int D, class E>
+__device__ __forceinline__ void store_rows(const ChunkArgs& a, int lane, int wave, int h, int row0, int R, int tile, int part, float m, float l,
+                                           f32x16 (&o)[D / 32]) {
+  const int half = lane >> 5, local = wave * 32 + (lane & 31), r = tile * kTile + local;
+  const float total = sum_over_halves(l);
+  const float inv = part >= 0 ? 1.0f : (m == -INFINITY ? 0.0f : a.c.gv / total);
+  if (r >= R) return;
+  const size_t at_part = (static_cast<size_t>(h) * a.parts + part) * kTile + local;
+  const size_t at_row = static_cast<size_t>(row0 + r / a.G) * a.Hq + h * a.G + r % a.G;
+#pragma unroll
+  for (int g = 0; g < 2; ++g)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // Positions c * D/16 .. of this lane.
+      const int c = 8 * g + 4 * half + i;
+      float x[D / 16];
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) x[j] = o[j / 2][8 * (j % 2) + 4 * g + i] * inv;
+      if (part >= 0) {
+#pragma unroll
+        for (int j = 0; j < D / 16; j += 4)
+          *reinterpret_cast<f32x4*>(a.part + at_part * D + c * (D / 16) + j) = f32x4{x[j], x[j + 1], x[j + 2], x[j + 3]};
+      } else {
+        uint16_t* dst = static_cast<uint16_t*>(a.out) + at_row * D + c * (D / 16);
+#pragma unroll
+        for (int j = 0; j < D / 16; j += 4)
+          *reinterpret_cast<u32x2*>(dst + j) = u32x2{elem_pack<E>(x[j], x[j + 1]), elem_pack<E>(x[j + 2], x[j + 3])};
+      }
+    }
+  if (half == 0) {
+    if (part >= 0) {
+      a.stat[at_part * 2] = m;
+      a.stat[at_part * 2 + 1] = total;
+    } else if (a.lse) {
+      a.lse[at_row] = m == -INFINITY && total == 0.0f ? -INFINITY : (m - kLift + __builtin_amdgcn_logf(total)) * kLn2;
+    }
+  }
 }
 
 template <int D>
@@ -358,8 +413,8 @@ template <int D, class E>
 __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkArgs a) {
   constexpr int kSteps = D / 16, DB = D / 32;
   constexpr int kGroup = D == 256 ? 1 : 2;  // tiles of 32 tokens at a time: the widest heads leave registers for one
-  // Without fences the scheduler loads many operands at once, for which they have none.
-  constexpr bool kFenced = D == 256, kWaits = D == 256;
+  constexpr bool kWaits = D == 256;
+  constexpr int kProducts = kGroup * (kSteps + 2 * DB), kAhead = D == 256 ? 3 : 6;
   __shared__ __align__(16) std::conditional_t<kWaits, Waiting, int> waiting;
   __shared__ __align__(16) Tile<D> tiles[2];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5, col = lane & 31;
@@ -419,6 +474,8 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) q[s] = __builtin_bit_cast(f16x8, w[s]);
     cm = fmaxf(a.scale * a.c.gk * kLog2e * factor, kMinNormal);
+    // The loop must not wait for these again, and with them for the next page.
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
   }
   float m = -INFINITY, l = 0.0f;
   f32x16 o[DB];
@@ -442,167 +499,154 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
     if constexpr (kWaits) waiting.load(block, wave, value, p, here());
     else raw.load(block, value, p, lane);
   };
-  const auto widen = [&](Tile<D>* to, int v) {
+  const auto widen = [&](Tile<D>* to, int v, int id) {
     const int lane = here();
     if constexpr (kWaits) raw = waiting.arrived(wave, lane);
     if (value) {
       uint32_t s = raw.scale;
-      if (!whole(view.page(v) * kPage, tile_least, tile_most)) s = note_bad<D>(s, to, p, lane);
+      if (!named(id) || !whole(view.page(v) * kPage, tile_least, tile_most)) s = note_bad<D>(s, to, p, lane);
       widen_values<D>(raw, s, to, p, lane);
     } else {
       widen_keys<D>(raw, to, p, lane);
     }
   };
-  if (threadIdx.x < 2 * kPage) tiles[threadIdx.x / kPage].bad[threadIdx.x % kPage] = 0u;
-  if (threadIdx.x < 2) tiles[threadIdx.x].any = 0u;
   int id = 0, next_id = 0, after_id = 0;  // of pages v, v + 1, v + 2
   if (v0 < v1) {
+    // The first products are of no weights with the values of no page.
+    for (int i = threadIdx.x; i < D * Tile<D>::kValueRow / 8; i += kThreads) *reinterpret_cast<u32x4*>(tiles[1].v + 8 * i) = u32x4{0u, 0u, 0u, 0u};
     id = page_id(v0);
     next_id = page_id(v0 + 1);
     load(id);
-    __syncthreads();
-    widen(&tiles[0], v0);
+    widen(&tiles[0], v0, id);
     load(next_id);
     after_id = page_id(v0 + 2);
   }
-  __syncthreads();
+  lds_barrier();
+  if (value) lds_barrier();
 
   const int key_row = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
+  f16x8 w[2 * kGroup];  // weights of the tokens before: none yet
+#pragma unroll
+  for (int i = 0; i < 2 * kGroup; ++i) w[i] = f16x8{};
+  int flagged = -1;      // the first slot of the page before, where it has NaN values that were noted
+  const auto add_values = [&](const Tile<D>& of, int u0) {
+#pragma unroll
+    for (int step = 0; step < 2 * kGroup; ++step)
+#pragma unroll
+      for (int d = 0; d < DB; ++d) {
+        const f16x8 x = *reinterpret_cast<const f16x8*>(of.v + (32 * d + col) * Tile<D>::kValueRow + 32 * u0 + 16 * step + 8 * half);
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, w[step], o[d], 0, 0, 0);
+      }
+  };
+  const auto add_scores = [&](const Tile<D>& of, int u0, f32x16 (&s)[kGroup]) {
+#pragma unroll
+    for (int u = 0; u < kGroup; ++u) s[u] = f32x16{};
+#pragma unroll
+    for (int step = 0; step < kSteps; ++step)
+#pragma unroll
+      for (int u = 0; u < kGroup; ++u) {
+        const f16x8 k = *reinterpret_cast<const f16x8*>(of.k + (32 * (u0 + u) + key_row) * Tile<D>::kKeyRow + 16 * step + 8 * half);
+        s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[step], s[u], 0, 0, 0);
+      }
+  };
+  // The rows that see a NaN value have it by hand.
+  const auto add_bad = [&](const Tile<D>& of) {
+    for (int t = 0; t < kPage; ++t) {
+      const uint32_t groups = of.any[t / 16] ? of.bad[t] : 0u;
+      const int slot = flagged + t;
+      if (groups && slot < limit && (!a.window || slot >= limit - a.window || slot < a.sinks)) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int row = 32 * d + 8 * (e / 4) + 4 * half + e % 4, position = (row % 16) * (D / 16) + row / 16;
+            if ((groups >> (position / 16)) & 1u) o[d][e] = NAN;
+          }
+      }
+    }
+  };
   for (int v = v0; v < v1; ++v) {
-    const Tile<D>& now = tiles[(v - v0) & 1];
+    const Tile<D>&now = tiles[(v - v0) & 1], &other = tiles[(v + 1 - v0) & 1];
     const int first = view.page(v) * kPage;
     const bool seen = named(id);
-    // Pages that no row of the wavefront sees cost it nothing but their widening.
     const bool work = busy && seen && first < wave_most && (!a.window || first + kPage > wave_least - a.window || first < a.sinks);
     const bool partial = work && !whole(first, wave_least, wave_most);
-    if (kFenced && v + 1 < v1) {
-      widen(&tiles[(v + 1 - v0) & 1], v + 1);
-      load(after_id);
-      __builtin_amdgcn_sched_barrier(0);
-    }
 #pragma unroll
     for (int u0 = 0; u0 < 2; u0 += kGroup) {
       f32x16 s[kGroup];
-      if (work) {
+      const Tile<D>& before = u0 ? now : other;
+      const int before_u0 = u0 ? u0 - kGroup : 2 - kGroup;
+      if (busy) {
+        add_values(before, before_u0);
+        add_scores(now, u0, s);
+        // The operands are read kAhead products before they are used: left to itself the compiler reads two,
+        // waits for them, and pays LDS's latency sixteen times.
+        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u) {
-          s[u] = f32x16{};
-#pragma unroll
-          for (int step = 0; step < kSteps; ++step) {
-            const f16x8 k = *reinterpret_cast<const f16x8*>(now.k + (32 * (u0 + u) + key_row) * Tile<D>::kKeyRow + 16 * step + 8 * half);
-            s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[step], s[u], 0, 0, 0);
-            if (kFenced && step % 4 == 3) __builtin_amdgcn_sched_barrier(0);
-          }
+        for (int i = 0; i < kProducts - kAhead; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
+        __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
       }
-      if (!kFenced && v + 1 < v1) {
-        widen(&tiles[(v + 1 - v0) & 1], v + 1);
-        load(after_id);
-      }
-      if (!work) continue;
-      if (partial) {
-        const int low = a.window ? limit - a.window : 0;
+      if (u0 == 0 && flagged >= 0) add_bad(other);
+      lds_barrier();
+      if (work) {
+        if (partial) {
+          const int low = a.window ? limit - a.window : 0;
+#pragma unroll
+          for (int u = 0; u < kGroup; ++u)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int slot = first + 32 * (u0 + u) + 16 * (e / 8) + 8 * half + e % 8;
+              const bool out = (slot >= limit) | ((slot < low) & (slot >= a.sinks));
+              s[u][e] = out ? -INFINITY : s[u][e];
+            }
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) top = fmaxf(top, s[u][e]);
+        top = max_over_halves(top) * cm;
+        const bool up = top > m + kSlack;
+        if (__any(up)) {
+          const float to = up ? top : m;
+          const float alpha = up ? __builtin_amdgcn_exp2f(m - to) : 1.0f;
+          m = to;
+          l *= alpha;
+#pragma unroll
+          for (int d = 0; d < DB; ++d) o[d] *= alpha;
+        }
+        const float lifted = m == -INFINITY ? 0.0f : m - kLift;
 #pragma unroll
         for (int u = 0; u < kGroup; ++u)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const int slot = first + 32 * (u0 + u) + 16 * (e / 8) + 8 * half + e % 8;
-            if (slot >= limit || (slot < low && slot >= a.sinks)) s[u][e] = -INFINITY;
+            const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][e], cm, -lifted));
+            l += x;
+            w[2 * u + e / 8][e % 8] = static_cast<_Float16>(x);
           }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2 * kGroup; ++i) w[i] = f16x8{};
       }
-      float top = s[0][0];
-#pragma unroll
-      for (int u = 0; u < kGroup; ++u)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, s[u][e]);
-      top = max_over_halves(top) * cm;
-      const bool up = top > m + kSlack;
-      if (__any(up)) {
-        const float to = up ? top : m;
-        const float alpha = up ? __builtin_amdgcn_exp2f(m - to) : 1.0f;
-        m = to;
-        l *= alpha;
-#pragma unroll
-        for (int d = 0; d < DB; ++d) o[d] *= alpha;
+      if (u0 == 0 && v + 1 < v1) {
+        widen(&tiles[(v + 1 - v0) & 1], v + 1, next_id);
+        load(after_id);
       }
-      const float lifted = m == -INFINITY ? 0.0f : m - kLift;
-      f16x8 w[2 * kGroup];
-#pragma unroll
-      for (int u = 0; u < kGroup; ++u)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][e], cm, -lifted));
-          l += x;
-          w[2 * u + e / 8][e % 8] = static_cast<_Float16>(x);
-        }
-#pragma unroll
-      for (int step = 0; step < 2 * kGroup; ++step)
-#pragma unroll
-        for (int d = 0; d < DB; ++d) {
-          const f16x8 x = *reinterpret_cast<const f16x8*>(now.v + (32 * d + col) * Tile<D>::kValueRow + 32 * u0 + 16 * step + 8 * half);
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, w[step], o[d], 0, 0, 0);
-          if (kFenced && d % 4 == 3) __builtin_amdgcn_sched_barrier(0);
-        }
+      lds_barrier();
     }
-    if (!whole(first, tile_least, tile_most) && now.any) {
-      // The rows that see a NaN value have it by hand.
-      for (int t = 0; t < kPage; ++t) {
-        const uint32_t groups = now.bad[t];
-        const int slot = first + t;
-        if (groups && seen && slot < limit && (!a.window || slot >= limit - a.window || slot < a.sinks)) {
-#pragma unroll
-          for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int row = 32 * d + 8 * (e / 4) + 4 * half + e % 4, position = (row % 16) * (D / 16) + row / 16;
-              if ((groups >> (position / 16)) & 1u) o[d][e] = NAN;
-            }
-        }
-      }
-      __syncthreads();
-      if (threadIdx.x < kPage) tiles[(v - v0) & 1].bad[threadIdx.x] = 0u;
-      if (threadIdx.x == 0) tiles[(v - v0) & 1].any = 0u;
-    }
+    flagged = -1;
+    if (seen && !whole(first, tile_least, tile_most) && (now.any[0] | now.any[1] | now.any[2] | now.any[3])) flagged = first;
     id = next_id;
     next_id = after_id;
     after_id = page_id(v + 3);
-    __syncthreads();
   }
-  if (r >= R) return;
-
-  const float total = sum_over_halves(l);
-  const float inv = part >= 0 ? 1.0f : (m == -INFINITY ? 0.0f : a.c.gv / total);
-  const int local = wave * 32 + col;
-  const size_t at_part = (static_cast<size_t>(h) * a.parts + part) * kTile + local;
-  const size_t at_row = static_cast<size_t>(row0 + r / a.G) * a.Hq + h * a.G + r % a.G;
-#pragma unroll
-  for (int g = 0; g < 2; ++g)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // Positions c * D/16 .. of this lane.
-      const int c = 8 * g + 4 * half + i;
-      float x[D / 16];
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) x[j] = o[j / 2][8 * (j % 2) + 4 * g + i] * inv;
-      if (part >= 0) {
-#pragma unroll
-        for (int j = 0; j < D / 16; j += 4)
-          *reinterpret_cast<f32x4*>(a.part + at_part * D + c * (D / 16) + j) = f32x4{x[j], x[j + 1], x[j + 2], x[j + 3]};
-      } else {
-        uint16_t* dst = static_cast<uint16_t*>(a.out) + at_row * D + c * (D / 16);
-#pragma unroll
-        for (int j = 0; j < D / 16; j += 4)
-          *reinterpret_cast<u32x2*>(dst + j) = u32x2{elem_pack<E>(x[j], x[j + 1]), elem_pack<E>(x[j + 2], x[j + 3])};
-      }
-    }
-  if (half == 0) {
-    if (part >= 0) {
-      a.stat[at_part * 2] = m;
-      a.stat[at_part * 2 + 1] = total;
-    } else if (a.lse) {
-      a.lse[at_row] = m == -INFINITY && total == 0.0f ? -INFINITY : (m - kLift + __builtin_amdgcn_logf(total)) * kLn2;
-    }
-  }
+  if (busy && v0 < v1) add_values(tiles[(v1 - 1 - v0) & 1], 2 - kGroup);
+  if (flagged >= 0) add_bad(tiles[(v1 - 1 - v0) & 1]);
+  if (!value) lds_barrier();
+  store_rows<D, E>(a, here(), wave, h, row0, R, tile, part, m, l, o);
 }
 
 // Adds the shares of split tiles: D / 4 threads have a row, eight shares' loads at a time.
