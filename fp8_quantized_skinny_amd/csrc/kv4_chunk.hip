@@ -98,6 +98,24 @@ __device__ __forceinline__ View view_of(const ChunkArgs& a, int len, int T, int 
   return v;
 }
 
+// Which pages rows with limits from `least` to `most` see: all of them the whole
+// of (each below end, and from begin on or below sinks), some of them something of.
+struct Sight {
+  int whole_begin, whole_end, whole_sinks, some_begin, some_end, some_sinks;
+  __device__ __forceinline__ Sight(const ChunkArgs& a, int least, int most)
+      : whole_begin(0), whole_end(least / kPage), whole_sinks(0), some_begin(0), some_end((most + kPage - 1) / kPage), some_sinks(0) {
+    if (a.window) {
+      const int last = most - a.window, first = least - a.window;  // where the latest and the earliest window begin
+      whole_begin = last > 0 ? (last + kPage - 1) / kPage : 0;
+      whole_sinks = a.sinks / kPage;
+      some_begin = first > 0 ? first / kPage : 0;
+      some_sinks = a.sinks / kPage + (a.sinks % kPage != 0);
+    }
+  }
+  __device__ __forceinline__ bool whole(int page) const { return page < whole_end && (page >= whole_begin || page < whole_sinks); }
+  __device__ __forceinline__ bool some(int page) const { return page < some_end && (page >= some_begin || page < some_sinks); }
+};
+
 // ---- the plan -----------------------------------------------------------------
 // One workgroup cuts every tile into shares of about equal numbers of pages, for
 // two shares per CU at least where there are pages for that; the longest tiles of
@@ -227,133 +245,134 @@ struct alignas(16) Tile {
   _Float16 k[kPage * kKeyRow];
   _Float16 v[D * kValueRow];
   uint32_t bad[kPage];  // groups of 16 positions of a token that are NaN and were made 0,
-  uint32_t any[4];      // where a tile of 16 tokens has one
+  uint32_t any[kWaves];  // where the wavefront that widened them found one
 };
 
-// A thread's part of a page: of tile p of 16 tokens, lane l of the first four
-// wavefronts has keys (token l % 16, quarter l / 16 of the positions), of the
-// others values (tokens 4 (l / 16) .. + 3, positions (l % 16) D/16 ..).
+// A thread's part of a page.  Wavefront 2 p + half has half of tile p of 16
+// tokens: lane l has, of the keys, of token l % 16 a half of quarter l / 16 of the
+// positions, and of the values tokens 4 (l / 16) + 2 half and the next at
+// positions (l % 16) D/16 ...  For both that is D/16 bytes of codes that lie
+// together, at the same place of the two parts of the block.
 template <int D>
-__device__ __forceinline__ const uint8_t* part_codes(const uint8_t* block, bool value, int p, int lane) {
-  return block + (value ? KvBlock<D>::kVCodes : 0) + (p * (D / 8) / 16) * 1024 + lane * 16 + p * (D / 8) % 16;
+__device__ __forceinline__ uint32_t code_at(int wave, int lane) {
+  const int run = wave * (D / 16);  // of the bytes of a lane
+  return run / 16 * 1024 + lane * 16 + run % 16;
+}
+// The two E4M3 scales of the values, and the one or, with the widest heads, two of the keys.
+template <int D>
+__device__ __forceinline__ uint32_t value_scale_at(int wave, int lane) {
+  return KvBlock<D>::kVScales + ((lane & 15) * D / 256) * 64 + (lane >> 4) * 16 + wave * 2;
 }
 template <int D>
-__device__ __forceinline__ const uint8_t* part_scales(const uint8_t* block, bool value, int p, int lane) {
-  return block + (value ? KvBlock<D>::kVScales + ((lane & 15) * D / 256) * 64 + (lane >> 4) * 16 + p * 4
-                        : KvBlock<D>::kKScales + lane * (D / 16) + p * (D / 64));
+__device__ __forceinline__ uint32_t key_scale_at(int wave, int lane) {
+  return KvBlock<D>::kKScales + lane * (D / 16) + wave * D / 128;
 }
 
 template <int D>
 struct Raw {
-  uint32_t w[D / 32];
-  uint32_t scale;
-  __device__ __forceinline__ void load(const uint8_t* block, bool value, int p, int lane) {
-    const uint8_t* s = part_codes<D>(block, value, p, lane);
+  static constexpr int kWords = D / 64;
+  uint32_t k[kWords], v[kWords], key_scale, value_scale;
+  static __device__ __forceinline__ void words(const uint8_t* s, uint32_t (&w)[kWords]) {
     if constexpr (D == 64) {
-      const u32x2 v = *reinterpret_cast<const u32x2*>(s);
-      w[0] = v.x;
-      w[1] = v.y;
+      w[0] = *reinterpret_cast<const uint32_t*>(s);
+    } else if constexpr (D == 128) {
+      const u32x2 x = *reinterpret_cast<const u32x2*>(s);
+      w[0] = x.x;
+      w[1] = x.y;
     } else {
+      const u32x4 x = *reinterpret_cast<const u32x4*>(s);
 #pragma unroll
-      for (int i = 0; i < D / 128; ++i) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(s + i * 1024);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[4 * i + j] = v[j];
-      }
+      for (int j = 0; j < 4; ++j) w[j] = x[j];
     }
-    const uint8_t* f = part_scales<D>(block, value, p, lane);
-    if (value || D == 256) scale = *reinterpret_cast<const uint32_t*>(f);
-    else if (D == 128) scale = *reinterpret_cast<const uint16_t*>(f);
-    else scale = *f;
+  }
+  __device__ __forceinline__ void load_keys(const uint8_t* block, int wave, int lane) {
+    words(block + code_at<D>(wave, lane), k);
+    const uint8_t* s = block + key_scale_at<D>(wave, lane);
+    if constexpr (D == 256) key_scale = *reinterpret_cast<const uint16_t*>(s);
+    else key_scale = *s;
+  }
+  __device__ __forceinline__ void load_values(const uint8_t* block, int wave, int lane) {
+    words(block + (KvBlock<D>::kVCodes + code_at<D>(wave, lane)), v);
+    value_scale = *reinterpret_cast<const uint16_t*>(block + value_scale_at<D>(wave, lane));
   }
 };
 
-// With the widest heads the next page's codes wait in LDS, each wavefront's own
-// apart: there are no registers for them beside the sums.
+// With the widest heads the next codes wait in LDS, each wavefront's own apart:
+// there are no registers for them beside the sums.  Scales come by dwords, of
+// which the wavefront has one half.
 struct Waiting {
   u32x4 codes[kWaves][2][64];
-  uint32_t scale[kWaves][64];
-  __device__ __forceinline__ void load(const uint8_t* block, int wave, bool value, int p, int lane) {
+  uint32_t scale[kWaves][2][64];
+  __device__ __forceinline__ void load_keys(const uint8_t* block, int wave, int lane) {
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));  // what was here has been read
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      __builtin_amdgcn_global_load_lds(part_codes<256>(block, value, p, lane) + i * 1024, &codes[wave][i][0], 16, 0, 0);
-    __builtin_amdgcn_global_load_lds(part_scales<256>(block, value, p, lane), &scale[wave][0], 4, 0, 0);
+    __builtin_amdgcn_global_load_lds(block + code_at<256>(wave, lane), &codes[wave][0][0], 16, 0, 0);
+    __builtin_amdgcn_global_load_lds(block + (key_scale_at<256>(wave, lane) & ~3u), &scale[wave][0][0], 4, 0, 0);
+  }
+  __device__ __forceinline__ void load_values(const uint8_t* block, int wave, int lane) {
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+    __builtin_amdgcn_global_load_lds(block + (KvBlock<256>::kVCodes + code_at<256>(wave, lane)), &codes[wave][1][0], 16, 0, 0);
+    __builtin_amdgcn_global_load_lds(block + (value_scale_at<256>(wave, lane) & ~3u), &scale[wave][1][0], 4, 0, 0);
   }
   __device__ __forceinline__ Raw<256> arrived(int wave, int lane) const {
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
     asm volatile("" ::: "memory");
     Raw<256> r;
+    const u32x4 k = codes[wave][0][lane], v = codes[wave][1][lane];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const u32x4 v = codes[wave][i][lane];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) r.w[4 * i + j] = v[j];
+    for (int j = 0; j < 4; ++j) {
+      r.k[j] = k[j];
+      r.v[j] = v[j];
     }
-    r.scale = scale[wave][lane];
+    r.key_scale = scale[wave][0][lane] >> (16 * (wave & 1));
+    r.value_scale = scale[wave][1][lane] >> (16 * (wave & 1));
     return r;
   }
 };
 
-template <int B>
-__device__ __forceinline__ f16x2 e2m1_of(uint32_t w) { return e2m1x2<B>(w); }
-__device__ __forceinline__ f16x2 e2m1_byte(uint32_t w, int b) {  // b: a constant after unrolling
-  return b == 0 ? e2m1_of<0>(w) : b == 1 ? e2m1_of<1>(w) : b == 2 ? e2m1_of<2>(w) : e2m1_of<3>(w);
+// Piece i of the widening of a thread's keys: eight positions.
+template <int D>
+__device__ __forceinline__ void widen_keys(const Raw<D>& r, _Float16* row, int i) {
+  const _Float16 s = e4m3x2<false>(r.key_scale)[i / 2];
+  *reinterpret_cast<f16x8*>(row + 8 * i) = e2m1x8(r.k[i]) * f16x8{s, s, s, s, s, s, s, s};
+}
+template <int D>
+__device__ __forceinline__ _Float16* key_row_of(Tile<D>* to, int wave, int lane) {
+  return to->k + (16 * (wave >> 1) + (lane & 15)) * Tile<D>::kKeyRow + (lane >> 4) * (D / 4) + (wave & 1) * (D / 8);
 }
 
+// Piece j of its values: position j of the D/16, two tokens.
 template <int D>
-__device__ __forceinline__ void widen_keys(const Raw<D>& r, Tile<D>* to, int p, int lane) {
-  _Float16* row = to->k + (16 * p + (lane & 15)) * Tile<D>::kKeyRow + (lane >> 4) * (D / 4);
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    const f16x2 pair = i / 4 ? e4m3x2<true>(r.scale) : e4m3x2<false>(r.scale);
-    const _Float16 s = pair[i / 2 % 2];
-    *reinterpret_cast<f16x8*>(row + 8 * i) = e2m1x8(r.w[i]) * f16x8{s, s, s, s, s, s, s, s};
-  }
-}
-
-template <int D>
-__device__ __forceinline__ void widen_values(const Raw<D>& r, uint32_t scale, Tile<D>* to, int p, int lane) {
+__device__ __forceinline__ void widen_values(const Raw<D>& r, _Float16* column, int j) {
   constexpr uint32_t kLow = 0x0F0F0F0Fu;
-  _Float16* col = to->v + (lane & 15) * Tile<D>::kValueRow + 16 * p + 4 * (lane >> 4);
-  const f16x2 s0 = e4m3x2<false>(scale), s1 = e4m3x2<true>(scale);
-#pragma unroll
-  for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
-    u32x2 pair[2];  // codes of two tokens, one byte per position: even positions in .x, odd ones in .y
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if constexpr (D == 64) {
-        pair[i] = u32x2{bits_of(kLow, r.w[i], r.w[i] >> 12), bits_of(kLow, r.w[i] >> 4, r.w[i] >> 16)};
-      } else {
-        const uint32_t a = r.w[2 * i * (D / 128) + half], b = r.w[(2 * i + 1) * (D / 128) + half];
-        pair[i] = u32x2{bits_of(kLow, a, b << 4), bits_of(kLow, a >> 4, b)};
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < (D == 64 ? 4 : 8); ++j) {
-      const f16x2 x = e2m1_byte(j % 2 ? pair[0].y : pair[0].x, j / 2) * s0, y = e2m1_byte(j % 2 ? pair[1].y : pair[1].x, j / 2) * s1;
-      *reinterpret_cast<f16x4*>(col + (half * 8 + j) * 16 * Tile<D>::kValueRow) = f16x4{x.x, x.y, y.x, y.y};
-    }
-  }
+  // Codes of the two tokens, one byte per position: even positions, then odd ones.
+  const uint32_t a = r.v[D == 64 ? 0 : j / 8], b = D == 64 ? a >> 16 : r.v[D == 64 ? 0 : D / 128 + j / 8];
+  const uint32_t pair = j % 2 ? bits_of(kLow, a >> 4, b) : bits_of(kLow, a, b << 4);
+  const int at = j % 8 / 2;
+  const f16x2 x = at == 0 ? e2m1x2<0>(pair) : at == 1 ? e2m1x2<1>(pair) : at == 2 ? e2m1x2<2>(pair) : e2m1x2<3>(pair);
+  *reinterpret_cast<f16x2*>(column + j * 16 * Tile<D>::kValueRow) = x * e4m3x2<false>(r.value_scale);
+}
+template <int D>
+__device__ __forceinline__ _Float16* value_column_of(Tile<D>* to, int wave, int lane) {
+  return to->v + (lane & 15) * Tile<D>::kValueRow + 8 * wave - 6 * (wave & 1) + 4 * (lane >> 4);
 }
 
 // Of a page that some row does not see whole, or that is none, NaN values become 0
 // and are noted: a weight of 0 must not carry them to the rows that do not see them.
 template <int D>
-__device__ __forceinline__ uint32_t note_bad(uint32_t scale, Tile<D>* to, int p, int lane) {
-  const uint32_t wrong = ((scale & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+__device__ __forceinline__ void note_bad(Raw<D>* r, Tile<D>* to, int wave, int lane) {
+  const uint32_t wrong = ((r->value_scale & 0x7F7Fu) + 0x0101u) & 0x8080u;
   const bool any = __any(wrong != 0u);
-  to->any[p] = any;
+  to->any[wave] = any;
   if (any) {
-    if (lane < 16) to->bad[16 * p + lane] = 0u;
+    uint32_t* bad = to->bad + 8 * wave - 6 * (wave & 1);  // of the wavefront's tokens
+    if (lane < 8) bad[4 * (lane >> 1) + (lane & 1)] = 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
       if ((wrong >> (8 * i + 7)) & 1u) {
-        scale &= ~(0xFFu << (8 * i));
-        atomicOr(&to->bad[16 * p + 4 * (lane >> 4) + i], 1u << ((lane & 15) * D / 256));
+        r->value_scale &= ~(0xFFu << (8 * i));
+        atomicOr(bad + 4 * (lane >> 4) + i, 1u << ((lane & 15) * D / 256));
       }
   }
-  return scale;
 }
 
 // A barrier for what went to LDS; loads of the next page stay in flight.
@@ -369,7 +388,7 @@ __device__ __forceinline__ void lds_barrier() {
 // A wavefront's rows, or its part of them where the tile is split.
 template <int D, class E>
 __device__ __forceinline__ void store_rows(const ChunkArgs& a, int lane, int wave, int h, int row0, int R, int tile, int part, float m, float l,
-                                           f32x16 (&o)[D / 32]) {
+                                           uint32_t nan_groups, f32x16 (&o)[D / 32]) {
   const int half = lane >> 5, local = wave * 32 + (lane & 31), r = tile * kTile + local;
   const float total = sum_over_halves(l);
   const float inv = part >= 0 ? 1.0f : (m == -INFINITY ? 0.0f : a.c.gv / total);
@@ -384,7 +403,7 @@ __device__ __forceinline__ void store_rows(const ChunkArgs& a, int lane, int wav
       const int c = 8 * g + 4 * half + i;
       float x[D / 16];
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) x[j] = o[j / 2][8 * (j % 2) + 4 * g + i] * inv;
+      for (int j = 0; j < D / 16; ++j) x[j] = (nan_groups >> (c * D / 256)) & 1u ? NAN : o[j / 2][8 * (j % 2) + 4 * g + i] * inv;
       if (part >= 0) {
 #pragma unroll
         for (int j = 0; j < D / 16; j += 4)
@@ -414,8 +433,10 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
   constexpr int kSteps = D / 16, DB = D / 32;
   constexpr int kGroup = D == 256 ? 1 : 2;  // tiles of 32 tokens at a time: the widest heads leave registers for one
   constexpr bool kWaits = D == 256;
-  constexpr int kProducts = kGroup * (kSteps + 2 * DB), kAhead = D == 256 ? 3 : 6;
+  constexpr int kValueProducts = 2 * kGroup * DB, kProducts = kValueProducts + kGroup * kSteps, kAhead = D == 256 ? 3 : 6;
+  constexpr int kPieces = D / 64 + D / 16;  // of a thread's widening: keys and values
   __shared__ __align__(16) std::conditional_t<kWaits, Waiting, int> waiting;
+  __shared__ uint32_t nan_groups[kTile];
   __shared__ __align__(16) Tile<D> tiles[2];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5, col = lane & 31;
   const int at = static_cast<int>(blockIdx.x) / a.c.Hk, h = static_cast<int>(blockIdx.x) % a.c.Hk;
@@ -435,10 +456,8 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
   const int tile_least = limit_at(tile * kTile), tile_most = limit_at(last);
   const int wave_least = busy ? limit_at(wave_row) : 0, wave_most = busy ? limit_at(wave_last) : 0;
   const int limit = r < R ? limit_at(r) : 0;
-  // Whether rows with limits from `least` to `most` all see the whole page from slot `first` on.
-  const auto whole = [&](int first, int least, int most) {
-    return first + kPage <= least && (!a.window || first >= most - a.window || first + kPage <= a.sinks);
-  };
+  // What these see of a page, by its number.
+  const Sight tile_sight(a, tile_least, tile_most), wave_sight(a, wave_least, wave_most);
 
   f16x8 q[kSteps];
   float cm;
@@ -482,9 +501,7 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
 #pragma unroll
   for (int d = 0; d < DB; ++d) o[d] = f32x16{};
 
-  // Thread's part of every page; a page that the table does not name is read as page 0 and seen by nobody.
-  const bool value = wave >= 4;
-  const int p = wave & 3;
+  // A page that the table does not name is read as the last one and seen by nobody.
   Raw<D> raw;
   // The lane, found again for each page where the addresses made of it would take registers all the while.
   const auto here = [&] {
@@ -494,103 +511,136 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
   };
   const auto named = [&](int id) { return static_cast<unsigned>(id) < static_cast<unsigned>(a.c.pages); };
   const auto page_id = [&](int v) { return uniform_load(table, view.page(v < v1 ? v : v1 - 1)); };
-  const auto load = [&](int id) {
-    const uint8_t* block = static_cast<const uint8_t*>(a.c.data) + (static_cast<size_t>(named(id) ? id : 0) * a.c.Hk + h) * KvBlock<D>::kBytes;
-    if constexpr (kWaits) waiting.load(block, wave, value, p, here());
-    else raw.load(block, value, p, lane);
+  const uint8_t* blocks = static_cast<const uint8_t*>(a.c.data) + static_cast<size_t>(h) * KvBlock<D>::kBytes;
+  const uint32_t page_bytes = static_cast<uint32_t>(a.c.Hk) * KvBlock<D>::kBytes;
+  const uint32_t last_page = static_cast<uint32_t>(a.c.pages) - 1u;
+  const auto block = [&](int id) {
+    const uint32_t n = static_cast<uint32_t>(id);
+    return blocks + static_cast<uint64_t>(page_bytes) * (n < last_page ? n : last_page);
   };
-  const auto widen = [&](Tile<D>* to, int v, int id) {
-    const int lane = here();
-    if constexpr (kWaits) raw = waiting.arrived(wave, lane);
-    if (value) {
-      uint32_t s = raw.scale;
-      if (!named(id) || !whole(view.page(v) * kPage, tile_least, tile_most)) s = note_bad<D>(s, to, p, lane);
-      widen_values<D>(raw, s, to, p, lane);
+  const auto load = [&](const uint8_t* keys, const uint8_t* values) {
+    const int l = here();
+    if constexpr (kWaits) {
+      waiting.load_keys(keys, wave, l);
+      waiting.load_values(values, wave, l);
     } else {
-      widen_keys<D>(raw, to, p, lane);
+      raw.load_keys(keys, wave, l);
+      raw.load_values(values, wave, l);
     }
   };
-  int id = 0, next_id = 0, after_id = 0;  // of pages v, v + 1, v + 2
+  if (half == 0) nan_groups[wave * 32 + col] = 0u;
+  int id = 0, next_id = 0, after_id = 0;  // of pages v, v + 1 and v + 2
   if (v0 < v1) {
     // The first products are of no weights with the values of no page.
     for (int i = threadIdx.x; i < D * Tile<D>::kValueRow / 8; i += kThreads) *reinterpret_cast<u32x4*>(tiles[1].v + 8 * i) = u32x4{0u, 0u, 0u, 0u};
     id = page_id(v0);
     next_id = page_id(v0 + 1);
-    load(id);
-    widen(&tiles[0], v0, id);
-    load(next_id);
     after_id = page_id(v0 + 2);
+    load(block(id), block(id));
+    if constexpr (kWaits) raw = waiting.arrived(wave, here());
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) widen_keys<D>(raw, key_row_of<D>(&tiles[0], wave, here()), i);
+    load(block(next_id), block(id));
   }
   lds_barrier();
-  if (value) lds_barrier();
+  if (wave >= kWaves / 2) lds_barrier();
 
   const int key_row = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
   f16x8 w[2 * kGroup];  // weights of the tokens before: none yet
 #pragma unroll
   for (int i = 0; i < 2 * kGroup; ++i) w[i] = f16x8{};
-  int flagged = -1;      // the first slot of the page before, where it has NaN values that were noted
-  const auto add_values = [&](const Tile<D>& of, int u0) {
-#pragma unroll
-    for (int step = 0; step < 2 * kGroup; ++step)
-#pragma unroll
-      for (int d = 0; d < DB; ++d) {
-        const f16x8 x = *reinterpret_cast<const f16x8*>(of.v + (32 * d + col) * Tile<D>::kValueRow + 32 * u0 + 16 * step + 8 * half);
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, w[step], o[d], 0, 0, 0);
-      }
+  int flagged = -1;  // the first slot of the page before, where NaN values of it may have been noted
+  // Operand i of a phase's products: the values of the tokens before, then the keys of these.
+  const auto operand = [&](const Tile<D>& before, int before_u0, const Tile<D>& now, int u0, int i) {
+    const int step = i / DB, d = i % DB, j = i - kValueProducts;
+    return *reinterpret_cast<const f16x8*>(
+        i < kValueProducts ? before.v + (32 * d + col) * Tile<D>::kValueRow + 32 * before_u0 + 16 * step + 8 * half
+                           : now.k + (32 * (u0 + j % kGroup) + key_row) * Tile<D>::kKeyRow + 16 * (j / kGroup) + 8 * half);
   };
-  const auto add_scores = [&](const Tile<D>& of, int u0, f32x16 (&s)[kGroup]) {
-#pragma unroll
-    for (int u = 0; u < kGroup; ++u) s[u] = f32x16{};
-#pragma unroll
-    for (int step = 0; step < kSteps; ++step)
-#pragma unroll
-      for (int u = 0; u < kGroup; ++u) {
-        const f16x8 k = *reinterpret_cast<const f16x8*>(of.k + (32 * (u0 + u) + key_row) * Tile<D>::kKeyRow + 16 * step + 8 * half);
-        s[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[step], s[u], 0, 0, 0);
-      }
-  };
-  // The rows that see a NaN value have it by hand.
+  const auto add_values = [&](f16x8 x, int i) { o[i % DB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, w[i / DB], o[i % DB], 0, 0, 0); };
+  // The groups of positions where this lane's row sees a NaN value of the page before are kept for the end.
   const auto add_bad = [&](const Tile<D>& of) {
+    uint32_t any = 0u, groups = 0u;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) any |= of.any[i];
+    if (!any) return;
     for (int t = 0; t < kPage; ++t) {
-      const uint32_t groups = of.any[t / 16] ? of.bad[t] : 0u;
       const int slot = flagged + t;
-      if (groups && slot < limit && (!a.window || slot >= limit - a.window || slot < a.sinks)) {
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int row = 32 * d + 8 * (e / 4) + 4 * half + e % 4, position = (row % 16) * (D / 16) + row / 16;
-            if ((groups >> (position / 16)) & 1u) o[d][e] = NAN;
-          }
-      }
+      if (of.any[t / 16 * 2 + t / 2 % 2] && slot < limit && (!a.window || slot >= limit - a.window || slot < a.sinks)) groups |= of.bad[t];
     }
+    if (half == 0) nan_groups[wave * 32 + col] |= groups;
   };
+  // The pages that all of the tile's rows see whole, most of them: view pages easy .. easy + easy_many.
+  const int easy = view.low + tile_sight.whole_begin - view.from;
+  const unsigned easy_many = tile_sight.whole_end > tile_sight.whole_begin ? tile_sight.whole_end - tile_sight.whole_begin : 0;
+
   for (int v = v0; v < v1; ++v) {
-    const Tile<D>&now = tiles[(v - v0) & 1], &other = tiles[(v + 1 - v0) & 1];
-    const int first = view.page(v) * kPage;
-    const bool seen = named(id);
-    const bool work = busy && seen && first < wave_most && (!a.window || first + kPage > wave_least - a.window || first < a.sinks);
-    const bool partial = work && !whole(first, wave_least, wave_most);
+    Tile<D>&now = tiles[(v - v0) & 1], &other = tiles[(v + 1 - v0) & 1];
+    int later_id = 0;
+    const bool whole = static_cast<unsigned>(v - easy) < easy_many && named(id);
+    bool work = busy, partial = false;
+    int first = 0;
+    if (flagged >= 0) add_bad(other);
+    flagged = -1;
+    if constexpr (kWaits) raw = waiting.arrived(wave, here());
+    if (!whole) {
+      const int page = view.page(v);
+      first = page * kPage;
+      work = busy && named(id) && wave_sight.some(page);
+      partial = work && !wave_sight.whole(page);
+      if (!named(id) || !tile_sight.whole(page)) note_bad<D>(&raw, &now, wave, here());
+      flagged = named(id) && !tile_sight.whole(page) ? first : -1;
+    }
 #pragma unroll
     for (int u0 = 0; u0 < 2; u0 += kGroup) {
       f32x16 s[kGroup];
-      const Tile<D>& before = u0 ? now : other;
-      const int before_u0 = u0 ? u0 - kGroup : 2 - kGroup;
-      if (busy) {
-        add_values(before, before_u0);
-        add_scores(now, u0, s);
-        // The operands are read kAhead products before they are used: left to itself the compiler reads two,
-        // waits for them, and pays LDS's latency sixteen times.
-        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
-#pragma unroll
-        for (int i = 0; i < kProducts - kAhead; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      // Keys are widened a page ahead; values, which the next phase's products want, of this one.
+      _Float16 *row = key_row_of<D>(&other, wave, here()), *column = value_column_of<D>(&now, wave, here());
+      const auto widen = [&](int i) {
+        if (i < kPieces) {
+          if (i < D / 64) widen_keys<D>(raw, row, i);
+          else widen_values<D>(raw, column, i - D / 64);
+        } else if (i == kPieces) {
+          load(block(after_id), block(next_id));
         }
-        __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
+      };
+      if (u0 == 0 && (kWaits || !busy)) {
+        // (Opaque, or the conversions would be taken out of both branches and done before the products.)
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) asm volatile("" : "+v"(raw.k[i]), "+v"(raw.v[i]));
+        asm volatile("" : "+v"(raw.key_scale), "+v"(raw.value_scale));
+#pragma unroll
+        for (int i = 0; i <= kPieces; ++i) {
+          widen(i);
+          __builtin_amdgcn_sched_barrier(0);  // one piece's registers at a time
+        }
       }
-      if (u0 == 0 && flagged >= 0) add_bad(other);
+      if (busy) {
+        // The operands are read kAhead products before they are used, and a piece of the widening follows each
+        // product: left to itself the compiler reads two operands, waits for them, and pays LDS's latency sixteen times.
+        const Tile<D>& before = u0 ? now : other;
+        const int before_u0 = u0 ? u0 - kGroup : 2 - kGroup;
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) s[u] = f32x16{};
+        f16x8 x[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) x[i] = operand(before, before_u0, now, u0, i);
+        __builtin_amdgcn_s_setprio(3);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < kProducts; ++i) {
+          const int j = i - kValueProducts;
+          if (i < kValueProducts) add_values(x[i % kAhead], i);
+          else s[j % kGroup] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[i % kAhead], q[j / kGroup], s[j % kGroup], 0, 0, 0);
+          if (i + kAhead < kProducts) x[i % kAhead] = operand(before, before_u0, now, u0, i + kAhead);
+          if (u0 == 0 && !kWaits) widen(i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_s_setprio(0);
+      }
       lds_barrier();
+      // (Here, since a load through the scalar cache and LDS reads wait for each other.)
+      if (u0 == 0) later_id = page_id(v + 3);
       if (work) {
         if (partial) {
           const int low = a.window ? limit - a.window : 0;
@@ -631,22 +681,20 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
 #pragma unroll
         for (int i = 0; i < 2 * kGroup; ++i) w[i] = f16x8{};
       }
-      if (u0 == 0 && v + 1 < v1) {
-        widen(&tiles[(v + 1 - v0) & 1], v + 1, next_id);
-        load(after_id);
-      }
       lds_barrier();
     }
-    flagged = -1;
-    if (seen && !whole(first, tile_least, tile_most) && (now.any[0] | now.any[1] | now.any[2] | now.any[3])) flagged = first;
     id = next_id;
     next_id = after_id;
-    after_id = page_id(v + 3);
+    after_id = later_id;
   }
-  if (busy && v0 < v1) add_values(tiles[(v1 - 1 - v0) & 1], 2 - kGroup);
+  if (busy && v0 < v1) {
+    const Tile<D>& last_tile = tiles[(v1 - 1 - v0) & 1];
+#pragma unroll
+    for (int i = 0; i < kValueProducts; ++i) add_values(operand(last_tile, 2 - kGroup, last_tile, 0, i), i);
+  }
   if (flagged >= 0) add_bad(tiles[(v1 - 1 - v0) & 1]);
-  if (!value) lds_barrier();
-  store_rows<D, E>(a, here(), wave, h, row0, R, tile, part, m, l, o);
+  if (wave < kWaves / 2) lds_barrier();
+  store_rows<D, E>(a, here(), wave, h, row0, R, tile, part, m, l, nan_groups[wave * 32 + (here() & 31)], o);
 }
 
 // Adds the shares of split tiles: D / 4 threads have a row, eight shares' loads at a time.
