@@ -245,94 +245,101 @@ struct alignas(16) Tile {
   _Float16 k[kPage * kKeyRow];
   _Float16 v[D * kValueRow];
   uint32_t bad[kPage];  // groups of 16 positions of a token that are NaN and were made 0,
-  uint32_t any[kWaves];  // where the wavefront that widened them found one
+  uint32_t any[4];      // where a tile of 16 tokens has one
 };
 
 // A thread's part of a page.  Wavefront 2 p + half has half of tile p of 16
 // tokens: lane l has, of the keys, of token l % 16 a half of quarter l / 16 of the
-// positions, and of the values tokens 4 (l / 16) + 2 half and the next at
-// positions (l % 16) D/16 ...  For both that is D/16 bytes of codes that lie
-// together, at the same place of the two parts of the block.
+// positions, D/16 bytes of codes that lie together; of the values, of tokens
+// 4 (l / 16) .. + 3 the even or the odd ones of the positions (l % 16) D/16 ..,
+// half of D/8 bytes that the other wavefront loads as well: four tokens at a time
+// go to LDS in half of the stores that two do.
 template <int D>
-__device__ __forceinline__ uint32_t code_at(int wave, int lane) {
+__device__ __forceinline__ uint32_t key_code_at(int wave, int lane) {
   const int run = wave * (D / 16);  // of the bytes of a lane
   return run / 16 * 1024 + lane * 16 + run % 16;
 }
-// The two E4M3 scales of the values, and the one or, with the widest heads, two of the keys.
+template <int D>
+__device__ __forceinline__ uint32_t value_code_at(int wave, int lane) {
+  const int run = (wave >> 1) * (D / 8);
+  return KvBlock<D>::kVCodes + run / 16 * 1024 + lane * 16 + run % 16;
+}
+// The four E4M3 scales of the values, and the one or, with the widest heads, two of the keys.
 template <int D>
 __device__ __forceinline__ uint32_t value_scale_at(int wave, int lane) {
-  return KvBlock<D>::kVScales + ((lane & 15) * D / 256) * 64 + (lane >> 4) * 16 + wave * 2;
+  return KvBlock<D>::kVScales + ((lane & 15) * D / 256) * 64 + (lane >> 4) * 16 + (wave >> 1) * 4;
 }
+// (Loaded by dwords: of bytes the compiler clears the upper bits as soon as they are there, and waits for that.)
 template <int D>
 __device__ __forceinline__ uint32_t key_scale_at(int wave, int lane) {
-  return KvBlock<D>::kKScales + lane * (D / 16) + wave * D / 128;
+  return KvBlock<D>::kKScales + lane * (D / 16) + (wave * D / 128 & ~3);
 }
+template <int D>
+__device__ __forceinline__ int key_scale_shift(int wave) { return (wave * D / 128 & 3) * 8; }
 
 template <int D>
 struct Raw {
-  static constexpr int kWords = D / 64;
-  uint32_t k[kWords], v[kWords], key_scale, value_scale;
-  static __device__ __forceinline__ void words(const uint8_t* s, uint32_t (&w)[kWords]) {
-    if constexpr (D == 64) {
-      w[0] = *reinterpret_cast<const uint32_t*>(s);
-    } else if constexpr (D == 128) {
-      const u32x2 x = *reinterpret_cast<const u32x2*>(s);
-      w[0] = x.x;
-      w[1] = x.y;
-    } else {
-      const u32x4 x = *reinterpret_cast<const u32x4*>(s);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = x[j];
-    }
-  }
+  uint32_t k[D / 64], v[D / 32], key_scale, value_scale;
   __device__ __forceinline__ void load_keys(const uint8_t* block, int wave, int lane) {
-    words(block + code_at<D>(wave, lane), k);
-    const uint8_t* s = block + key_scale_at<D>(wave, lane);
-    if constexpr (D == 256) key_scale = *reinterpret_cast<const uint16_t*>(s);
-    else key_scale = *s;
+    const uint8_t* c = block + key_code_at<D>(wave, lane);
+    if constexpr (D == 64) {
+      k[0] = *reinterpret_cast<const uint32_t*>(c);
+    } else {
+      const u32x2 x = *reinterpret_cast<const u32x2*>(c);
+      k[0] = x.x;
+      k[1] = x.y;
+    }
+    key_scale = *reinterpret_cast<const uint32_t*>(block + key_scale_at<D>(wave, lane));
   }
   __device__ __forceinline__ void load_values(const uint8_t* block, int wave, int lane) {
-    words(block + (KvBlock<D>::kVCodes + code_at<D>(wave, lane)), v);
-    value_scale = *reinterpret_cast<const uint16_t*>(block + value_scale_at<D>(wave, lane));
+    const uint8_t* c = block + value_code_at<D>(wave, lane);
+    if constexpr (D == 64) {
+      const u32x2 x = *reinterpret_cast<const u32x2*>(c);
+      v[0] = x.x;
+      v[1] = x.y;
+    } else {
+      const u32x4 x = *reinterpret_cast<const u32x4*>(c);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = x[j];
+    }
+    value_scale = *reinterpret_cast<const uint32_t*>(block + value_scale_at<D>(wave, lane));
   }
 };
 
-// With the widest heads the next codes wait in LDS, each wavefront's own apart:
-// there are no registers for them beside the sums.  Scales come by dwords, of
-// which the wavefront has one half.
+// With the widest heads the next codes wait in LDS: there are no registers for
+// them beside the sums.  The two wavefronts of a tile load one half of its values
+// each, so what they wait for has to lie before a barrier (see the loop).
 struct Waiting {
-  u32x4 codes[kWaves][2][64];
-  uint32_t scale[kWaves][2][64];
-  __device__ __forceinline__ void load_keys(const uint8_t* block, int wave, int lane) {
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));  // what was here has been read
-    __builtin_amdgcn_global_load_lds(block + code_at<256>(wave, lane), &codes[wave][0][0], 16, 0, 0);
-    __builtin_amdgcn_global_load_lds(block + (key_scale_at<256>(wave, lane) & ~3u), &scale[wave][0][0], 4, 0, 0);
+  u32x4 keys[kWaves][64], values[kWaves][64];
+  uint32_t key_scale[kWaves][64], value_scale[kWaves / 2][64];
+  __device__ __forceinline__ void load(const uint8_t* key_block, const uint8_t* value_block, int wave, int lane) {
+    __builtin_amdgcn_global_load_lds(key_block + key_code_at<256>(wave, lane), &keys[wave][0], 16, 0, 0);
+    __builtin_amdgcn_global_load_lds(key_block + key_scale_at<256>(wave, lane), &key_scale[wave][0], 4, 0, 0);
+    __builtin_amdgcn_global_load_lds(value_block + (value_code_at<256>(wave, lane) + (wave & 1) * 1024), &values[wave][0], 16, 0, 0);
+    __builtin_amdgcn_global_load_lds(value_block + value_scale_at<256>(wave, lane), &value_scale[wave >> 1][0], 4, 0, 0);
   }
-  __device__ __forceinline__ void load_values(const uint8_t* block, int wave, int lane) {
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
-    __builtin_amdgcn_global_load_lds(block + (KvBlock<256>::kVCodes + code_at<256>(wave, lane)), &codes[wave][1][0], 16, 0, 0);
-    __builtin_amdgcn_global_load_lds(block + (value_scale_at<256>(wave, lane) & ~3u), &scale[wave][1][0], 4, 0, 0);
-  }
-  __device__ __forceinline__ Raw<256> arrived(int wave, int lane) const {
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
-    asm volatile("" ::: "memory");
-    Raw<256> r;
-    const u32x4 k = codes[wave][0][lane], v = codes[wave][1][lane];
+  __device__ __forceinline__ void arrived(Raw<256>* r, int wave, int lane) const {
+    const u32x4 k = keys[wave][lane];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      r.k[j] = k[j];
-      r.v[j] = v[j];
+    for (int j = 0; j < 4; ++j) r->k[j] = k[j];
+    r->key_scale = key_scale[wave][lane];
+    r->value_scale = value_scale[wave >> 1][lane];
+  }
+  // Of the values the words for the first or the second eight positions.
+  __device__ __forceinline__ void arrived_values(Raw<256>* r, int half, int wave, int lane) const {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&values[t ? wave | 1 : wave & ~1][lane]);
+      r->v[4 * t + half] = w[half];
+      r->v[4 * t + 2 + half] = w[2 + half];
     }
-    r.key_scale = scale[wave][0][lane] >> (16 * (wave & 1));
-    r.value_scale = scale[wave][1][lane] >> (16 * (wave & 1));
-    return r;
   }
 };
 
 // Piece i of the widening of a thread's keys: eight positions.
 template <int D>
-__device__ __forceinline__ void widen_keys(const Raw<D>& r, _Float16* row, int i) {
-  const _Float16 s = e4m3x2<false>(r.key_scale)[i / 2];
+__device__ __forceinline__ void widen_keys(const Raw<D>& r, _Float16* row, int wave, int i) {
+  const _Float16 s = e4m3x2<false>(r.key_scale >> key_scale_shift<D>(wave))[i / 2];
   *reinterpret_cast<f16x8*>(row + 8 * i) = e2m1x8(r.k[i]) * f16x8{s, s, s, s, s, s, s, s};
 }
 template <int D>
@@ -340,38 +347,43 @@ __device__ __forceinline__ _Float16* key_row_of(Tile<D>* to, int wave, int lane)
   return to->k + (16 * (wave >> 1) + (lane & 15)) * Tile<D>::kKeyRow + (lane >> 4) * (D / 4) + (wave & 1) * (D / 8);
 }
 
-// Piece j of its values: position j of the D/16, two tokens.
+// Piece i of its values: position 2 i or 2 i + 1 of the D/16, four tokens.
 template <int D>
-__device__ __forceinline__ void widen_values(const Raw<D>& r, _Float16* column, int j) {
-  constexpr uint32_t kLow = 0x0F0F0F0Fu;
-  // Codes of the two tokens, one byte per position: even positions, then odd ones.
-  const uint32_t a = r.v[D == 64 ? 0 : j / 8], b = D == 64 ? a >> 16 : r.v[D == 64 ? 0 : D / 128 + j / 8];
-  const uint32_t pair = j % 2 ? bits_of(kLow, a >> 4, b) : bits_of(kLow, a, b << 4);
-  const int at = j % 8 / 2;
-  const f16x2 x = at == 0 ? e2m1x2<0>(pair) : at == 1 ? e2m1x2<1>(pair) : at == 2 ? e2m1x2<2>(pair) : e2m1x2<3>(pair);
-  *reinterpret_cast<f16x2*>(column + j * 16 * Tile<D>::kValueRow) = x * e4m3x2<false>(r.value_scale);
+__device__ __forceinline__ void widen_values(const Raw<D>& r, _Float16* column, int wave, int i) {
+  const int odd = 4 * (wave & 1);
+  f16x2 x[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    // Codes of two tokens, one byte for each of the positions.
+    const uint32_t a = r.v[D == 64 ? t : 2 * t * (D / 128) + i / 4];
+    const uint32_t b = D == 64 ? a >> 16 : r.v[D == 64 ? 0 : (2 * t + 1) * (D / 128) + i / 4];
+    const uint32_t pair = bits_of(0x0F0F0F0Fu, a >> odd, b << (4 - odd));
+    const int at = i % 4;
+    const f16x2 c = at == 0 ? e2m1x2<0>(pair) : at == 1 ? e2m1x2<1>(pair) : at == 2 ? e2m1x2<2>(pair) : e2m1x2<3>(pair);
+    x[t] = c * (t ? e4m3x2<true>(r.value_scale) : e4m3x2<false>(r.value_scale));
+  }
+  *reinterpret_cast<f16x4*>(column + i * 32 * Tile<D>::kValueRow) = f16x4{x[0].x, x[0].y, x[1].x, x[1].y};
 }
 template <int D>
 __device__ __forceinline__ _Float16* value_column_of(Tile<D>* to, int wave, int lane) {
-  return to->v + (lane & 15) * Tile<D>::kValueRow + 8 * wave - 6 * (wave & 1) + 4 * (lane >> 4);
+  return to->v + ((lane & 15) + 16 * (wave & 1)) * Tile<D>::kValueRow + 16 * (wave >> 1) + 4 * (lane >> 4);
 }
 
 // Of a page that some row does not see whole, or that is none, NaN values become 0
 // and are noted: a weight of 0 must not carry them to the rows that do not see them.
 template <int D>
 __device__ __forceinline__ void note_bad(Raw<D>* r, Tile<D>* to, int wave, int lane) {
-  const uint32_t wrong = ((r->value_scale & 0x7F7Fu) + 0x0101u) & 0x8080u;
+  const uint32_t wrong = ((r->value_scale & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  r->value_scale &= ~(wrong | (wrong - (wrong >> 7)));
+  if (wave & 1) return;  // the other wavefront of the tile sees the same
+  const int p = wave >> 1;
   const bool any = __any(wrong != 0u);
-  to->any[wave] = any;
+  to->any[p] = any;
   if (any) {
-    uint32_t* bad = to->bad + 8 * wave - 6 * (wave & 1);  // of the wavefront's tokens
-    if (lane < 8) bad[4 * (lane >> 1) + (lane & 1)] = 0u;
+    if (lane < 16) to->bad[16 * p + lane] = 0u;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if ((wrong >> (8 * i + 7)) & 1u) {
-        r->value_scale &= ~(0xFFu << (8 * i));
-        atomicOr(bad + 4 * (lane >> 4) + i, 1u << ((lane & 15) * D / 256));
-      }
+    for (int i = 0; i < 4; ++i)
+      if ((wrong >> (8 * i + 7)) & 1u) atomicOr(&to->bad[16 * p + 4 * (lane >> 4) + i], 1u << ((lane & 15) * D / 256));
   }
 }
 
@@ -434,7 +446,7 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
   constexpr int kGroup = D == 256 ? 1 : 2;  // tiles of 32 tokens at a time: the widest heads leave registers for one
   constexpr bool kWaits = D == 256;
   constexpr int kValueProducts = 2 * kGroup * DB, kProducts = kValueProducts + kGroup * kSteps, kAhead = D == 256 ? 3 : 6;
-  constexpr int kPieces = D / 64 + D / 16;  // of a thread's widening: keys and values
+  constexpr int kPieces = D / 64 + D / 32;  // of a thread's widening: keys and values
   __shared__ __align__(16) std::conditional_t<kWaits, Waiting, int> waiting;
   __shared__ uint32_t nan_groups[kTile];
   __shared__ __align__(16) Tile<D> tiles[2];
@@ -456,9 +468,6 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
   const int tile_least = limit_at(tile * kTile), tile_most = limit_at(last);
   const int wave_least = busy ? limit_at(wave_row) : 0, wave_most = busy ? limit_at(wave_last) : 0;
   const int limit = r < R ? limit_at(r) : 0;
-  // What these see of a page, by its number.
-  const Sight tile_sight(a, tile_least, tile_most), wave_sight(a, wave_least, wave_most);
-
   f16x8 q[kSteps];
   float cm;
   {
@@ -510,7 +519,11 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
     return l;
   };
   const auto named = [&](int id) { return static_cast<unsigned>(id) < static_cast<unsigned>(a.c.pages); };
-  const auto page_id = [&](int v) { return uniform_load(table, view.page(v < v1 ? v : v1 - 1)); };
+  // Ids of the next view pages, one a lane: now those of v_ids .., then the 64 after these.  (Loads through the scalar
+  // cache would wait for LDS reads and these for them.)
+  const auto ids_of = [&](int v) { return v0 < v1 ? table[view.page(v + lane < v1 ? v + lane : v1 - 1)] : 0; };
+  int v_ids = v0, ids = ids_of(v0), more_ids = ids_of(v0 + 64);
+  const auto page_id = [&](int v) { return __builtin_amdgcn_readlane(ids, v - v_ids); };
   const uint8_t* blocks = static_cast<const uint8_t*>(a.c.data) + static_cast<size_t>(h) * KvBlock<D>::kBytes;
   const uint32_t page_bytes = static_cast<uint32_t>(a.c.Hk) * KvBlock<D>::kBytes;
   const uint32_t last_page = static_cast<uint32_t>(a.c.pages) - 1u;
@@ -521,14 +534,18 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
   const auto load = [&](const uint8_t* keys, const uint8_t* values) {
     const int l = here();
     if constexpr (kWaits) {
-      waiting.load_keys(keys, wave, l);
-      waiting.load_values(values, wave, l);
+      waiting.load(keys, values, wave, l);
     } else {
       raw.load_keys(keys, wave, l);
       raw.load_values(values, wave, l);
     }
   };
   if (half == 0) nan_groups[wave * 32 + col] = 0u;
+  // A barrier at which what waits in LDS has arrived.
+  const auto arrive = [] {
+    if constexpr (kWaits) __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
+    lds_barrier();
+  };
   int id = 0, next_id = 0, after_id = 0;  // of pages v, v + 1 and v + 2
   if (v0 < v1) {
     // The first products are of no weights with the values of no page.
@@ -537,12 +554,16 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
     next_id = page_id(v0 + 1);
     after_id = page_id(v0 + 2);
     load(block(id), block(id));
-    if constexpr (kWaits) raw = waiting.arrived(wave, here());
+    if constexpr (kWaits) {
+      arrive();
+      waiting.arrived(&raw, wave, here());
+    }
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) widen_keys<D>(raw, key_row_of<D>(&tiles[0], wave, here()), i);
+    for (int i = 0; i < D / 64; ++i) widen_keys<D>(raw, key_row_of<D>(&tiles[0], wave, here()), wave, i);
+    if constexpr (kWaits) arrive();  // what was waiting has been read
     load(block(next_id), block(id));
   }
-  lds_barrier();
+  arrive();
   if (wave >= kWaves / 2) lds_barrier();
 
   const int key_row = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
@@ -562,17 +583,18 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
   const auto add_bad = [&](const Tile<D>& of) {
     uint32_t any = 0u, groups = 0u;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) any |= of.any[i];
+    for (int i = 0; i < 4; ++i) any |= of.any[i];
     if (!any) return;
     for (int t = 0; t < kPage; ++t) {
       const int slot = flagged + t;
-      if (of.any[t / 16 * 2 + t / 2 % 2] && slot < limit && (!a.window || slot >= limit - a.window || slot < a.sinks)) groups |= of.bad[t];
+      if (of.any[t / 16] && slot < limit && (!a.window || slot >= limit - a.window || slot < a.sinks)) groups |= of.bad[t];
     }
     if (half == 0) nan_groups[wave * 32 + col] |= groups;
   };
   // The pages that all of the tile's rows see whole, most of them: view pages easy .. easy + easy_many.
-  const int easy = view.low + tile_sight.whole_begin - view.from;
-  const unsigned easy_many = tile_sight.whole_end > tile_sight.whole_begin ? tile_sight.whole_end - tile_sight.whole_begin : 0;
+  const Sight whole_tile(a, tile_least, tile_most);
+  const int easy = view.low + whole_tile.whole_begin - view.from;
+  const unsigned easy_many = whole_tile.whole_end > whole_tile.whole_begin ? whole_tile.whole_end - whole_tile.whole_begin : 0;
 
   for (int v = v0; v < v1; ++v) {
     Tile<D>&now = tiles[(v - v0) & 1], &other = tiles[(v + 1 - v0) & 1];
@@ -582,14 +604,20 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
     int first = 0;
     if (flagged >= 0) add_bad(other);
     flagged = -1;
-    if constexpr (kWaits) raw = waiting.arrived(wave, here());
+    if constexpr (kWaits) waiting.arrived(&raw, wave, here());
     if (!whole) {
+      // (Found for each such page, of which there are few: kept, all this takes more scalar registers than there are.)
+      int limits[4] = {tile_least, tile_most, wave_least, wave_most};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) asm volatile("" : "+s"(limits[i]));
+      const Sight tile_sight(a, limits[0], limits[1]), wave_sight(a, limits[2], limits[3]);
       const int page = view.page(v);
+      const bool noted = !named(id) || !tile_sight.whole(page);
       first = page * kPage;
       work = busy && named(id) && wave_sight.some(page);
       partial = work && !wave_sight.whole(page);
-      if (!named(id) || !tile_sight.whole(page)) note_bad<D>(&raw, &now, wave, here());
-      flagged = named(id) && !tile_sight.whole(page) ? first : -1;
+      if (noted) note_bad<D>(&raw, &now, wave, here());
+      flagged = noted && named(id) ? first : -1;
     }
 #pragma unroll
     for (int u0 = 0; u0 < 2; u0 += kGroup) {
@@ -598,23 +626,26 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
       _Float16 *row = key_row_of<D>(&other, wave, here()), *column = value_column_of<D>(&now, wave, here());
       const auto widen = [&](int i) {
         if (i < kPieces) {
-          if (i < D / 64) widen_keys<D>(raw, row, i);
-          else widen_values<D>(raw, column, i - D / 64);
-        } else if (i == kPieces) {
-          load(block(after_id), block(next_id));
+          if (i < D / 64) widen_keys<D>(raw, row, wave, i);
+          else widen_values<D>(raw, column, wave, i - D / 64);
         }
       };
-      if (u0 == 0 && (kWaits || !busy)) {
+      const auto widen_alone = [&] {
         // (Opaque, or the conversions would be taken out of both branches and done before the products.)
+        if constexpr (!kWaits) {
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) asm volatile("" : "+v"(raw.k[i]), "+v"(raw.v[i]));
-        asm volatile("" : "+v"(raw.key_scale), "+v"(raw.value_scale));
+          for (int i = 0; i < D / 64; ++i) asm volatile("" : "+v"(raw.k[i]), "+v"(raw.v[i]), "+v"(raw.v[D / 64 + i]));
+        }
 #pragma unroll
-        for (int i = 0; i <= kPieces; ++i) {
+        for (int i = 0; i < kPieces; ++i) {
+          if constexpr (kWaits) {
+            if (i == D / 64 || i == D / 64 + 4) waiting.arrived_values(&raw, i == D / 64 ? 0 : 1, wave, here());
+          }
           widen(i);
           __builtin_amdgcn_sched_barrier(0);  // one piece's registers at a time
         }
-      }
+      };
+      if (u0 == 0 && kWaits) widen_alone();
       if (busy) {
         // The operands are read kAhead products before they are used, and a piece of the widening follows each
         // product: left to itself the compiler reads two operands, waits for them, and pays LDS's latency sixteen times.
@@ -637,19 +668,31 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
           __builtin_amdgcn_sched_barrier(0);
         }
         __builtin_amdgcn_s_setprio(0);
+      } else if (u0 == 0 && !kWaits) {
+        widen_alone();
       }
       lds_barrier();
-      // (Here, since a load through the scalar cache and LDS reads wait for each other.)
-      if (u0 == 0) later_id = page_id(v + 3);
+      if (u0 == 0) {
+        if (v + 3 - v_ids == 64) {
+          v_ids += 64;
+          ids = more_ids;
+          more_ids = ids_of(v_ids + 64);
+        }
+        later_id = page_id(v + 3);
+      }
+      if (u0 == 0) load(block(after_id), block(next_id));
       if (work) {
         if (partial) {
-          const int low = a.window ? limit - a.window : 0;
+          // Slots counted from the lane's first.  (Opaque, or its differences to the 32 tokens are kept all the while.)
+          int until = limit - first - 32 * u0 - 8 * half;
+          asm volatile("" : "+v"(until));
+          const int from = a.window ? (until > 0 ? until : 0) - a.window : -kPage, sunk = a.sinks - first - 32 * u0 - 8 * half;
 #pragma unroll
           for (int u = 0; u < kGroup; ++u)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const int slot = first + 32 * (u0 + u) + 16 * (e / 8) + 8 * half + e % 8;
-              const bool out = (slot >= limit) | ((slot < low) & (slot >= a.sinks));
+              const int slot = 32 * u + 16 * (e / 8) + e % 8;
+              const bool out = (slot >= until) | ((slot < from) & (slot >= sunk));
               s[u][e] = out ? -INFINITY : s[u][e];
             }
         }
@@ -681,7 +724,8 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
 #pragma unroll
         for (int i = 0; i < 2 * kGroup; ++i) w[i] = f16x8{};
       }
-      lds_barrier();
+      if (u0 + kGroup == 2) arrive();
+      else lds_barrier();
     }
     id = next_id;
     next_id = after_id;
