@@ -29,8 +29,8 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kTile = 32 * kWaves;
-constexpr int kSlots = 256;       // workgroups that the CUs hold at once
-constexpr int kLeast = 16;        // fewest pages of a share of a split tile
+constexpr int kSlots = 256;  // workgroups that the CUs hold at once
+constexpr int kLeast = 16;   // fewest pages of a workgroup where tiles are cut
 constexpr int kPlanThreads = 1024;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -40,15 +40,15 @@ constexpr float kMinNormal = 0x1p-126f;
 // kv4_attention.hip): below 2^14, and exact to 2^-11 down to 2^-20 of the greatest.
 constexpr float kLift = 6.0f, kSlack = 8.0f;
 
-// A tile's share of the pages that its rows see: view pages v0 .. v1.
-struct Share {
+// A piece of the work: view pages v0 .. v1 of those that a tile's rows see.
+struct Piece {
   int b, first, T, tile;  // sequence, its first row and number of them, tile of it
   int v0, v1;
-  int part;               // its place among the parts of split tiles, -1: it is the whole tile
+  int part;               // its place among the parts of cut tiles, -1: it is the whole tile
   int pad;
 };
-struct Split {            // a tile of several shares
-  int first, T, tile, part, shares;
+struct Cut {              // a tile of several pieces
+  int first, T, tile, part, pieces;
 };
 
 struct ChunkArgs {
@@ -58,15 +58,16 @@ struct ChunkArgs {
   const int32_t* starts;
   void* out;
   float* lse;
-  int* counts;          // [2]: shares, split tiles
+  int* counts;          // [2]: workgroups per head, cut tiles
   int* begin;           // [B + 1]: first row of each sequence
   int* offset;          // [B]: tiles before each sequence
-  Share* share;
-  Split* split;
+  int* first;           // [workgroup + 1]: its first piece
+  Piece* piece;
+  Cut* cut;
   float* stat;          // [head][part][kTile][2]: reference maximum (log2) and sum
   float* part;          // [head][part][kTile][D]
   int64_t parts;        // per head
-  int N, Hq, G, tiles;  // tiles: most that N rows of B sequences make
+  int N, Hq, G;
   int window, sinks;
   float scale;
 };
@@ -117,21 +118,30 @@ struct Sight {
 };
 
 // ---- the plan -----------------------------------------------------------------
-// One workgroup cuts every tile into shares of about equal numbers of pages, for
-// two shares per CU at least where there are pages for that; the longest tiles of
-// a sequence, its last, come first.
+// One workgroup lists the pieces of a head's work, the same for all heads.  Where
+// there are many tiles, none of them long, a workgroup of the attention has a
+// whole tile, the longest of a sequence, its last, first.  Otherwise the pages of
+// all tiles in a row are dealt out evenly to as many workgroups as the CUs hold:
+// each has the end of one tile, whole ones, and the beginning of another, and no
+// CU waits for a last long tile (512 tokens over 120000, 24 tiles of 1883 pages a
+// head: 1754 us with each tile in six equal shares, TODO so).
 //
 // The rows of a sequence go from its start to the next one's; a start that is not
 // in 0 .. N counts as the nearer of these, and one below an earlier start as that:
 // no two sequences have a row in common, whatever the starts are.
-__device__ __forceinline__ int block_scan(int v, int* total) {
-  __shared__ int sums[kPlanThreads / 64];
+template <class I>
+__device__ __forceinline__ I block_scan(I v, I* total) {
+  __shared__ I sums[kPlanThreads / 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int in = wave_scan(v);
+  I in = v;
+  for (int o = 1; o < 64; o <<= 1) {
+    const I x = __shfl_up(in, o);
+    if (lane >= o) in += x;
+  }
   __syncthreads();
   if (lane == 63) sums[wave] = in;
   __syncthreads();
-  int before = 0, all = 0;
+  I before = 0, all = 0;
   for (int w = 0; w < kPlanThreads / 64; ++w) {
     before += w < wave ? sums[w] : 0;
     all += sums[w];
@@ -139,6 +149,8 @@ __device__ __forceinline__ int block_scan(int v, int* total) {
   *total = all;
   return before + in - v;
 }
+
+__host__ __device__ constexpr int slots_per_head(int Hk) { return kSlots / Hk > 1 ? kSlots / Hk : 1; }
 
 // The greatest of the threads' values up to this one's.
 __device__ __forceinline__ int block_running_max(int v) {
@@ -157,8 +169,12 @@ __device__ __forceinline__ int block_running_max(int v) {
 
 __global__ __launch_bounds__(kPlanThreads) void chunk_plan(const ChunkArgs a) {
   __shared__ unsigned long long pages;
+  __shared__ int longest;
   const int tid = threadIdx.x;
-  if (tid == 0) pages = 0ull;
+  if (tid == 0) {
+    pages = 0ull;
+    longest = 0;
+  }
   for (int b0 = 0, top = 0; b0 <= a.c.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
     int s = b <= a.c.B ? a.starts[b] : 0;
@@ -179,7 +195,7 @@ __global__ __launch_bounds__(kPlanThreads) void chunk_plan(const ChunkArgs a) {
     tiles += all;
   }
   __syncthreads();
-  const auto find = [&](int i, Share* s) {  // the sequence and tile of tile i, and its pages
+  const auto find = [&](int i, Piece* s) {  // the sequence and tile of tile i, and its pages
     int lo = 0, hi = a.c.B - 1;             // the last sequence whose offset is i or less
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
@@ -192,34 +208,52 @@ __global__ __launch_bounds__(kPlanThreads) void chunk_plan(const ChunkArgs a) {
     s->tile = tiles_of(s->T) - 1 - (i - a.offset[lo]);
     return view_of(a, kv_len(a.c, lo), s->T, s->tile).pages();
   };
-  Share s;
+  // A tile whose rows see nothing counts as one page.
+  Piece s;
   unsigned long long mine = 0ull;
-  for (int i = tid; i < tiles; i += kPlanThreads) mine += find(i, &s);
+  int top = 0;
+  for (int i = tid; i < tiles; i += kPlanThreads) {
+    const int n = find(i, &s);
+    mine += n ? n : 1;
+    top = n > top ? n : top;
+  }
   atomicAdd(&pages, mine);
+  atomicMax(&longest, top);
   __syncthreads();
-  const unsigned long long even = (pages * a.c.Hk + 2 * kSlots - 1) / (2 * kSlots);
-  const int most = static_cast<int>(even < kLeast ? kLeast : (even < 0x7FFFFFFFull ? even : 0x7FFFFFFFull));
-  int shares = 0, parts = 0, splits = 0;
+  const long long all_pages = static_cast<long long>(pages), slots = slots_per_head(a.c.Hk);
+  const bool whole = slots < 4 || (static_cast<long long>(tiles) >= 4 * slots && longest * 2 * slots <= all_pages);
+  const long long even = (all_pages + slots - 1) / slots, each = whole ? 1 : (even < kLeast ? kLeast : even);
+  int pieces = 0, parts = 0, cuts = 0;
+  long long before = 0;
   for (int i0 = 0; i0 < tiles; i0 += kPlanThreads) {
     const int i = i0 + tid, n = i < tiles ? find(i, &s) : 0;
-    const int k = i < tiles ? (n > most ? (n - 1) / most + 1 : 1) : 0;
-    int all, all_parts, all_splits;
-    const int at = shares + block_scan(k, &all), part = parts + block_scan(k > 1 ? k : 0, &all_parts);
-    const int split = splits + block_scan(k > 1 ? 1 : 0, &all_splits);
+    const long long size = i < tiles ? (whole || !n ? 1 : n) : 0;
+    long long all_sizes;
+    const long long p0 = before + block_scan<long long>(size, &all_sizes), p1 = p0 + size;
+    const long long j0 = p0 / each, j1 = (p1 - 1) / each;  // its workgroups
+    const int k = i < tiles ? static_cast<int>(j1 - j0) + 1 : 0;
+    int all, all_parts, all_cuts;
+    const int at = pieces + block_scan<int>(k, &all), part = parts + block_scan<int>(k > 1 ? k : 0, &all_parts);
+    const int cut = cuts + block_scan<int>(k > 1 ? 1 : 0, &all_cuts);
     for (int j = 0; j < k; ++j) {
-      s.v0 = static_cast<int>(static_cast<int64_t>(n) * j / k);
-      s.v1 = static_cast<int>(static_cast<int64_t>(n) * (j + 1) / k);
+      const long long from = (j0 + j) * each, to = from + each;
+      s.v0 = j ? static_cast<int>(from - p0) : 0;
+      s.v1 = j + 1 < k ? static_cast<int>(to - p0) : n;
       s.part = k > 1 ? part + j : -1;
-      a.share[at + j] = s;
+      a.piece[at + j] = s;
+      if (from >= p0) a.first[j0 + j] = at + j;
     }
-    if (k > 1) a.split[split] = Split{s.first, s.T, s.tile, part, k};
-    shares += all;
+    if (k > 1) a.cut[cut] = Cut{s.first, s.T, s.tile, part, k};
+    before += all_sizes;
+    pieces += all;
     parts += all_parts;
-    splits += all_splits;
+    cuts += all_cuts;
   }
   if (tid == 0) {
-    a.counts[0] = shares;
-    a.counts[1] = splits;
+    const int groups = static_cast<int>((before + each - 1) / each);
+    a.first[groups] = pieces;
+    a.counts[0] = groups;
+    a.counts[1] = cuts;
   }
 }
 
@@ -437,23 +471,35 @@ __device__ __forceinline__ void store_rows(const ChunkArgs& a, int lane, int wav
   }
 }
 
+// The kernel's arguments, read again: those that are seldom needed would take
+// scalar registers from the loop, and these vector registers.
+__device__ __forceinline__ const ChunkArgs& arguments() {
+  auto p = (const __attribute__((address_space(4))) ChunkArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const ChunkArgs*)p;
+}
+
 template <int D>
-constexpr int chunk_waves() { return 2; }  // per SIMD
+struct Shared {
+  Tile<D> tiles[2];
+  std::conditional_t<D == 256, Waiting, int> waiting;
+  uint32_t nan_groups[kTile];
+};
 
 template <int D, class E>
-__global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkArgs a) {
+__device__ __forceinline__ void attend_piece(const ChunkArgs& a, int h, int at, Shared<D>& shared) {
   constexpr int kSteps = D / 16, DB = D / 32;
   constexpr int kGroup = D == 256 ? 1 : 2;  // tiles of 32 tokens at a time: the widest heads leave registers for one
   constexpr bool kWaits = D == 256;
   constexpr int kValueProducts = 2 * kGroup * DB, kProducts = kValueProducts + kGroup * kSteps, kAhead = D == 256 ? 3 : 6;
   constexpr int kPieces = D / 64 + D / 32;  // of a thread's widening: keys and values
-  __shared__ __align__(16) std::conditional_t<kWaits, Waiting, int> waiting;
-  __shared__ uint32_t nan_groups[kTile];
-  __shared__ __align__(16) Tile<D> tiles[2];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5, col = lane & 31;
-  const int at = static_cast<int>(blockIdx.x) / a.c.Hk, h = static_cast<int>(blockIdx.x) % a.c.Hk;
-  if (at >= uniform_load(a.counts, 0)) return;
-  const int32_t* words = reinterpret_cast<const int32_t*>(a.share + at);
+  Tile<D>(&tiles)[2] = shared.tiles;
+  auto& waiting = shared.waiting;
+  auto& nan_groups = shared.nan_groups;
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));  // what is made of it is made for each piece again, or takes registers in between
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5, col = lane & 31;
+  const int32_t* words = reinterpret_cast<const int32_t*>(a.piece + at);
   const int b = uniform_load(words, 0), row0 = uniform_load(words, 1), T = uniform_load(words, 2), tile = uniform_load(words, 3),
             v0 = uniform_load(words, 4), v1 = uniform_load(words, 5), part = uniform_load(words, 6);
   const int len = kv_len_uniform(a.c, b), R = T * a.G;  // at most N * G, which an int holds
@@ -549,7 +595,9 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
   int id = 0, next_id = 0, after_id = 0;  // of pages v, v + 1 and v + 2
   if (v0 < v1) {
     // The first products are of no weights with the values of no page.
-    for (int i = threadIdx.x; i < D * Tile<D>::kValueRow / 8; i += kThreads) *reinterpret_cast<u32x4*>(tiles[1].v + 8 * i) = u32x4{0u, 0u, 0u, 0u};
+    uint32_t zero = 0u;
+    asm volatile("" : "+v"(zero));
+    for (int i = threadIdx.x; i < D * Tile<D>::kValueRow / 8; i += kThreads) *reinterpret_cast<u32x4*>(tiles[1].v + 8 * i) = u32x4{zero, zero, zero, zero};
     id = page_id(v0);
     next_id = page_id(v0 + 1);
     after_id = page_id(v0 + 2);
@@ -585,6 +633,7 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
 #pragma unroll
     for (int i = 0; i < 4; ++i) any |= of.any[i];
     if (!any) return;
+    const ChunkArgs& a = arguments();
     for (int t = 0; t < kPage; ++t) {
       const int slot = flagged + t;
       if (of.any[t / 16] && slot < limit && (!a.window || slot >= limit - a.window || slot < a.sinks)) groups |= of.bad[t];
@@ -610,6 +659,7 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
       int limits[4] = {tile_least, tile_most, wave_least, wave_most};
 #pragma unroll
       for (int i = 0; i < 4; ++i) asm volatile("" : "+s"(limits[i]));
+      const ChunkArgs& a = arguments();
       const Sight tile_sight(a, limits[0], limits[1]), wave_sight(a, limits[2], limits[3]);
       const int page = view.page(v);
       const bool noted = !named(id) || !tile_sight.whole(page);
@@ -683,6 +733,7 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
       if (u0 == 0) load(block(after_id), block(next_id));
       if (work) {
         if (partial) {
+          const ChunkArgs& a = arguments();
           // Slots counted from the lane's first.  (Opaque, or its differences to the 32 tokens are kept all the while.)
           int until = limit - first - 32 * u0 - 8 * half;
           asm volatile("" : "+v"(until));
@@ -738,34 +789,46 @@ __global__ __launch_bounds__(kThreads, chunk_waves<D>()) void chunk(const ChunkA
   }
   if (flagged >= 0) add_bad(tiles[(v1 - 1 - v0) & 1]);
   if (wave < kWaves / 2) lds_barrier();
-  store_rows<D, E>(a, here(), wave, h, row0, R, tile, part, m, l, nan_groups[wave * 32 + (here() & 31)], o);
+  store_rows<D, E>(arguments(), here(), wave, h, row0, R, tile, part, m, l, nan_groups[wave * 32 + (here() & 31)], o);
 }
 
-// Adds the shares of split tiles: D / 4 threads have a row, eight shares' loads at a time.
+template <int D, class E>
+__global__ __launch_bounds__(kThreads, 2) void chunk(const ChunkArgs a) {
+  __shared__ __align__(16) Shared<D> shared;
+  const int at = static_cast<int>(blockIdx.x) / a.c.Hk, h = static_cast<int>(blockIdx.x) % a.c.Hk;
+  if (at >= uniform_load(a.counts, 0)) return;
+  const int begin = uniform_load(a.first, at), end = uniform_load(a.first, at + 1);
+  for (int p = begin; p < end; ++p) {
+    if (p > begin) lds_barrier();  // all have done with the tiles of the piece before
+    attend_piece<D, E>(arguments(), h, p, shared);
+  }
+}
+
+// Adds the pieces of cut tiles: D / 4 threads have a row, eight pieces' loads at a time.
 template <int D, class E>
 __global__ __launch_bounds__(256) void chunk_join(const ChunkArgs a) {
   constexpr int kPer = D / 4, kRows = 256 / kPer, kBatch = 8;
   const int at = static_cast<int>(blockIdx.x) / a.c.Hk, h = static_cast<int>(blockIdx.x) % a.c.Hk;
   if (at >= uniform_load(a.counts, 1)) return;
-  const Split sp = a.split[at];
+  const Cut sp = a.cut[at];
   const int local = blockIdx.y * kRows + threadIdx.x / kPer, r = sp.tile * kTile + local, pos = threadIdx.x % kPer * 4;
   if (r >= sp.T * a.G) return;
   float mm = -INFINITY, total = 0.0f;
   f32x4 x{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s0 = 0; s0 < sp.shares; s0 += kBatch) {
+  for (int s0 = 0; s0 < sp.pieces; s0 += kBatch) {
     float2 st[kBatch];
     f32x4 v[kBatch];
 #pragma unroll
     for (int s = 0; s < kBatch; ++s) {
-      const int share = s0 + s < sp.shares ? s0 + s : s0;
-      const size_t p = (static_cast<size_t>(h) * a.parts + sp.part + share) * kTile + local;
+      const int piece = s0 + s < sp.pieces ? s0 + s : s0;
+      const size_t p = (static_cast<size_t>(h) * a.parts + sp.part + piece) * kTile + local;
       st[s] = *reinterpret_cast<const float2*>(a.stat + p * 2);
       v[s] = *reinterpret_cast<const f32x4*>(a.part + p * D + pos);
     }
 #pragma unroll
     for (int s = 0; s < kBatch; ++s)
-      if (s0 + s < sp.shares) {
-        // A share without weight is zeros; one with nothing but NaN scores has the same
+      if (s0 + s < sp.pieces) {
+        // A piece without weight is zeros; one with nothing but NaN scores has the same
         // maximum, -inf, but a NaN sum: both are added, times 0.
         const float to = fmaxf(mm, st[s].x), about = to == -INFINITY ? 0.0f : to;
         const float f0 = __builtin_amdgcn_exp2f(mm - about), f = __builtin_amdgcn_exp2f(st[s].x - about);
@@ -795,19 +858,19 @@ ChunkPlan kv4_chunk_plan(int N, int B, int Hq, int Hk, int D, int width, int win
     const int64_t seen = (window + tokens) / kPage + 2 + (static_cast<int64_t>(sinks) + kPage - 1) / kPage;
     pages = seen < pages ? seen : pages;
   }
-  // A tile is split when it has more than `most` pages, of which there are 2 * kSlots / Hk
-  // (and a part of one) among the pages of a head's tiles.
-  const int64_t most = 2 * kSlots / Hk + 1;
-  p.splits = pages > kLeast ? (p.tiles < most ? p.tiles : most) : 0;
-  const int64_t each = p.splits * ((pages + kLeast - 1) / kLeast);
-  p.parts = p.splits + most < each ? p.splits + most : each;
-  p.shares = p.tiles + (p.parts > 0 ? p.parts : 0);
+  // Of g workgroups in a row at most g - 1 begin inside a tile, and each of these cuts makes one piece more.
+  const int64_t slots = slots_per_head(Hk), even = (p.tiles * pages + kLeast - 1) / kLeast;
+  const int64_t inside = slots < 4 ? 0 : (slots < even ? slots : even) - 1;
+  p.cuts = p.tiles < inside ? p.tiles : inside;
+  p.parts = p.cuts + inside;
+  p.groups = p.tiles > inside + 1 ? p.tiles : inside + 1;
   p.counts_off = kSyncBytes;
   p.begin_off = p.counts_off + 256;
   p.offset_off = p.begin_off + up(static_cast<size_t>(B + 1) * 4);
-  p.share_off = p.offset_off + up(static_cast<size_t>(B) * 4);
-  p.split_off = p.share_off + up(static_cast<size_t>(p.shares) * sizeof(Share));
-  p.stat_off = p.split_off + up(static_cast<size_t>(p.splits) * sizeof(Split));
+  p.first_off = p.offset_off + up(static_cast<size_t>(B) * 4);
+  p.piece_off = p.first_off + up(static_cast<size_t>(p.groups + 1) * 4);
+  p.cut_off = p.piece_off + up(static_cast<size_t>(p.tiles + inside) * sizeof(Piece));
+  p.stat_off = p.cut_off + up(static_cast<size_t>(p.cuts) * sizeof(Cut));
   p.part_off = p.stat_off + static_cast<size_t>(Hk) * p.parts * kTile * 8;
   p.total = p.part_off + static_cast<size_t>(Hk) * p.parts * kTile * D * 4;
   return p;
@@ -818,14 +881,15 @@ hipError_t launch_kv4_chunk(const kv4_cache& c, const void* q, int64_t row, int6
   const ChunkPlan p = kv4_chunk_plan(N, c.B, Hq, c.Hk, c.D, c.width, window, sinks);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const ChunkArgs a{c, static_cast<const uint16_t*>(q), row, head, starts, out, lse, reinterpret_cast<int*>(ws + p.counts_off),
-                    reinterpret_cast<int*>(ws + p.begin_off), reinterpret_cast<int*>(ws + p.offset_off), reinterpret_cast<Share*>(ws + p.share_off),
-                    reinterpret_cast<Split*>(ws + p.split_off), reinterpret_cast<float*>(ws + p.stat_off),
-                    reinterpret_cast<float*>(ws + p.part_off), p.parts, N, Hq, Hq / c.Hk, static_cast<int>(p.tiles), window, sinks, scale};
+                    reinterpret_cast<int*>(ws + p.begin_off), reinterpret_cast<int*>(ws + p.offset_off), reinterpret_cast<int*>(ws + p.first_off),
+                    reinterpret_cast<Piece*>(ws + p.piece_off), reinterpret_cast<Cut*>(ws + p.cut_off),
+                    reinterpret_cast<float*>(ws + p.stat_off), reinterpret_cast<float*>(ws + p.part_off), p.parts, N, Hq, Hq / c.Hk,
+                    window, sinks, scale};
   chunk_plan<<<1, kPlanThreads, 0, stream>>>(a);
   const auto run = [&](auto d, auto e) {
-    chunk<d(), decltype(e)><<<dim3(static_cast<unsigned>(p.shares * c.Hk)), kThreads, 0, stream>>>(a);
-    if (p.splits)
-      chunk_join<d(), decltype(e)><<<dim3(static_cast<unsigned>(p.splits * c.Hk), kTile * d() / 1024), 256, 0, stream>>>(a);
+    chunk<d(), decltype(e)><<<dim3(static_cast<unsigned>(p.groups * c.Hk)), kThreads, 0, stream>>>(a);
+    if (p.cuts)
+      chunk_join<d(), decltype(e)><<<dim3(static_cast<unsigned>(p.cuts * c.Hk), kTile * d() / 1024), 256, 0, stream>>>(a);
   };
   const auto by_type = [&](auto d) {
     if (type == SKINNY_F16) run(d, F16());

@@ -124,7 +124,7 @@ int check_chunk(int N, int B, int Hq, int Hk, int D, int width) {
   if (N < 1 || Hq < 1 || Hq % Hk != 0 || Hq / Hk > SKINNY_KV_MAX_GROUP) return SKINNY_ESHAPE;
   return static_cast<int64_t>(N) * (Hq / Hk) <= INT32_MAX ? SKINNY_OK : SKINNY_ESHAPE;
 }
-bool chunk_fits(const ChunkPlan& p, int Hk) { return p.tiles < (int64_t{1} << 30) && fits_grid(p.shares * Hk, 512); }
+bool chunk_fits(const ChunkPlan& p, int Hk) { return p.tiles < (int64_t{1} << 30) && fits_grid(p.groups * Hk, 512); }
 
 // [B][T][H][D] views of 16-bit elements, for qk_norm_rope.
 struct Heads {

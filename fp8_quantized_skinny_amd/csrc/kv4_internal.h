@@ -33,11 +33,11 @@ hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type,
                                 int sinks, void* out, float* lse, void* workspace, hipStream_t stream);
 hipError_t launch_kv4_weights(const kv4_cache& c, const kv4_rows& q, int type, int T, int Hq, float scale,
                               const float* lse, const float* acc, float* acc_out, hipStream_t stream);
-// How a chunk call is laid out: the most tiles of rows, tiles that are split, parts
-// of them and shares, each per key/value head, and the workspace.
+// How a chunk call is laid out: the most tiles of rows, workgroups, tiles that are
+// cut and parts of them, each per key/value head, and the workspace.
 struct ChunkPlan {
-  int64_t tiles, splits, parts, shares;
-  size_t counts_off, begin_off, offset_off, share_off, split_off, stat_off, part_off, total;
+  int64_t tiles, groups, cuts, parts;
+  size_t counts_off, begin_off, offset_off, first_off, piece_off, cut_off, stat_off, part_off, total;
 };
 ChunkPlan kv4_chunk_plan(int N, int B, int Hq, int Hk, int D, int width, int window, int sinks);
 hipError_t launch_kv4_chunk(const kv4_cache& c, const void* q, int64_t row, int64_t head, const int32_t* starts, int N,
