@@ -31,7 +31,8 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kTile = 32 * kWaves;
 constexpr int kSlots = 256;  // workgroups that the CUs hold at once
 constexpr int kLeast = 16;   // fewest pages of a workgroup where tiles are cut
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 256;
+constexpr int kPlanHeld = 1024;  // sequences whose rows and tiles the plan keeps in LDS
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kMinNormal = 0x1p-126f;
@@ -129,32 +130,44 @@ struct Sight {
 // The rows of a sequence go from its start to the next one's; a start that is not
 // in 0 .. N counts as the nearer of these, and one below an earlier start as that:
 // no two sequences have a row in common, whatever the starts are.
-template <class I>
-__device__ __forceinline__ I block_scan(I v, I* total) {
-  __shared__ I sums[kPlanThreads / 64];
+constexpr int kPlanWaves = kPlanThreads / 64;
+
+// Sums over the threads before this one, and over all, of each of N values.
+template <class I, int N>
+__device__ __forceinline__ void block_scan(I (&v)[N], I (&total)[N]) {
+  __shared__ I sums[N][kPlanWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  I in = v;
-  for (int o = 1; o < 64; o <<= 1) {
-    const I x = __shfl_up(in, o);
-    if (lane >= o) in += x;
+  I own[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    own[i] = v[i];
+    for (int o = 1; o < 64; o <<= 1) {
+      const I x = __shfl_up(v[i], o);
+      if (lane >= o) v[i] += x;
+    }
   }
   __syncthreads();
-  if (lane == 63) sums[wave] = in;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (lane == 63) sums[i][wave] = v[i];
   __syncthreads();
-  I before = 0, all = 0;
-  for (int w = 0; w < kPlanThreads / 64; ++w) {
-    before += w < wave ? sums[w] : 0;
-    all += sums[w];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    total[i] = 0;
+    v[i] -= own[i];
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) {
+      v[i] += w < wave ? sums[i][w] : 0;
+      total[i] += sums[i][w];
+    }
   }
-  *total = all;
-  return before + in - v;
 }
 
 __host__ __device__ constexpr int slots_per_head(int Hk) { return kSlots / Hk > 1 ? kSlots / Hk : 1; }
 
-// The greatest of the threads' values up to this one's.
-__device__ __forceinline__ int block_running_max(int v) {
-  __shared__ int tops[kPlanThreads / 64];
+// The greatest of the threads' values up to this one's, and of all.
+__device__ __forceinline__ int block_running_max(int v, int* all) {
+  __shared__ int tops[kPlanWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int o = 1; o < 64; o <<= 1) {
     const int x = __shfl_up(v, o);
@@ -163,95 +176,117 @@ __device__ __forceinline__ int block_running_max(int v) {
   __syncthreads();
   if (lane == 63) tops[wave] = v;
   __syncthreads();
+  int top = tops[0];
+#pragma unroll
+  for (int w = 1; w < kPlanWaves; ++w) top = tops[w] > top ? tops[w] : top;
   for (int w = 0; w < wave; ++w) v = tops[w] > v ? tops[w] : v;
+  *all = top;
   return v;
 }
 
 __global__ __launch_bounds__(kPlanThreads) void chunk_plan(const ChunkArgs a) {
-  __shared__ unsigned long long pages;
-  __shared__ int longest;
-  const int tid = threadIdx.x;
-  if (tid == 0) {
-    pages = 0ull;
-    longest = 0;
-  }
-  for (int b0 = 0, top = 0; b0 <= a.c.B; b0 += kPlanThreads) {
+  __shared__ int held_begin[kPlanHeld + 1], held_offset[kPlanHeld], held_len[kPlanHeld];
+  const int tid = threadIdx.x, B = a.c.B;
+  const bool held = B <= kPlanHeld;
+  for (int b0 = 0, top = 0; b0 <= B; b0 += kPlanThreads) {
     const int b = b0 + tid;
-    int s = b <= a.c.B ? a.starts[b] : 0;
+    int s = b <= B ? a.starts[b] : 0;
+    if (held && b < B) held_len[b] = kv_len(a.c, b);
     s = s < top ? top : s;
     s = s > a.N ? a.N : s;
-    s = block_running_max(s);
-    if (b <= a.c.B) a.begin[b] = s;
-    __syncthreads();
-    top = a.begin[b0 + kPlanThreads - 1 < a.c.B ? b0 + kPlanThreads - 1 : a.c.B];
+    s = block_running_max(s, &top);
+    if (b <= B) (held ? held_begin[b] : a.begin[b]) = s;
   }
+  __syncthreads();
+  const auto begin_of = [&](int b) { return held ? held_begin[b] : a.begin[b]; };
   const auto tiles_of = [&](int T) { return static_cast<int>((static_cast<int64_t>(T) * a.G + kTile - 1) / kTile); };
   int tiles = 0;
-  for (int b0 = 0; b0 < a.c.B; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
     const int b = b0 + tid;
-    int all;
-    const int at = block_scan(b < a.c.B ? tiles_of(a.begin[b + 1] - a.begin[b]) : 0, &all);
-    if (b < a.c.B) a.offset[b] = tiles + at;
-    tiles += all;
+    int n[1] = {b < B ? tiles_of(begin_of(b + 1) - begin_of(b)) : 0}, all[1];
+    block_scan(n, all);
+    if (b < B) (held ? held_offset[b] : a.offset[b]) = tiles + n[0];
+    tiles += all[0];
   }
   __syncthreads();
   const auto find = [&](int i, Piece* s) {  // the sequence and tile of tile i, and its pages
-    int lo = 0, hi = a.c.B - 1;             // the last sequence whose offset is i or less
+    int lo = 0, hi = B - 1;                 // the last sequence whose offset is i or less
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
-      if (a.offset[mid] <= i) lo = mid;
+      if ((held ? held_offset[mid] : a.offset[mid]) <= i) lo = mid;
       else hi = mid - 1;
     }
     s->b = lo;
-    s->first = a.begin[lo];
-    s->T = a.begin[lo + 1] - s->first;
-    s->tile = tiles_of(s->T) - 1 - (i - a.offset[lo]);
-    return view_of(a, kv_len(a.c, lo), s->T, s->tile).pages();
+    s->first = begin_of(lo);
+    s->T = begin_of(lo + 1) - s->first;
+    s->tile = tiles_of(s->T) - 1 - (i - (held ? held_offset[lo] : a.offset[lo]));
+    return view_of(a, held ? held_len[lo] : kv_len(a.c, lo), s->T, s->tile).pages();
   };
   // A tile whose rows see nothing counts as one page.
-  Piece s;
-  unsigned long long mine = 0ull;
-  int top = 0;
-  for (int i = tid; i < tiles; i += kPlanThreads) {
-    const int n = find(i, &s);
-    mine += n ? n : 1;
-    top = n > top ? n : top;
-  }
-  atomicAdd(&pages, mine);
-  atomicMax(&longest, top);
-  __syncthreads();
-  const long long all_pages = static_cast<long long>(pages), slots = slots_per_head(a.c.Hk);
-  const bool whole = slots < 4 || (static_cast<long long>(tiles) >= 4 * slots && longest * 2 * slots <= all_pages);
-  const long long even = (all_pages + slots - 1) / slots, each = whole ? 1 : (even < kLeast ? kLeast : even);
-  int pieces = 0, parts = 0, cuts = 0;
-  long long before = 0;
+  Piece s{};
+  long long pages = 0, before[1] = {0};  // of all tiles; of those before the thread's last
+  int longest = 0, n = 0;
   for (int i0 = 0; i0 < tiles; i0 += kPlanThreads) {
-    const int i = i0 + tid, n = i < tiles ? find(i, &s) : 0;
-    const long long size = i < tiles ? (whole || !n ? 1 : n) : 0;
-    long long all_sizes;
-    const long long p0 = before + block_scan<long long>(size, &all_sizes), p1 = p0 + size;
-    const long long j0 = p0 / each, j1 = (p1 - 1) / each;  // its workgroups
+    const int i = i0 + tid;
+    n = i < tiles ? find(i, &s) : 0;
+    int top;
+    block_running_max(n, &top);
+    longest = top > longest ? top : longest;
+    long long all[1];
+    before[0] = i < tiles ? (n ? n : 1) : 0;
+    block_scan(before, all);
+    before[0] += pages;
+    pages += all[0];
+  }
+  const long long slots = slots_per_head(a.c.Hk);
+  const bool whole = slots < 4 || (static_cast<long long>(tiles) >= 4 * slots && longest * 2 * slots <= pages);
+  const long long even = (pages + slots - 1) / slots, each = even < kLeast ? kLeast : even;
+  int pieces = 0, parts = 0, cuts = 0;
+  long long done = 0;
+  for (int i0 = 0; i0 < tiles; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    if (whole) {
+      if (i < tiles) {
+        s.v1 = find(i, &s);
+        s.v0 = 0;
+        s.part = -1;
+        a.piece[i] = s;
+        a.first[i] = i;
+      }
+      continue;
+    }
+    if (tiles > kPlanThreads) {  // otherwise known from before
+      n = i < tiles ? find(i, &s) : 0;
+      long long all[1];
+      before[0] = i < tiles ? (n ? n : 1) : 0;
+      block_scan(before, all);
+      before[0] += done;
+      done += all[0];
+    }
+    const long long p0 = before[0], p1 = p0 + (n ? n : 1);
+    // Its workgroups; in 32 bits wherever the pages are counted in those, which a division takes a tenth of the time for.
+    const bool few = pages <= 0x7FFFFFFF;
+    const long long j0 = few ? static_cast<uint32_t>(p0) / static_cast<uint32_t>(each) : p0 / each;
+    const long long j1 = few ? static_cast<uint32_t>(p1 - 1) / static_cast<uint32_t>(each) : (p1 - 1) / each;
     const int k = i < tiles ? static_cast<int>(j1 - j0) + 1 : 0;
-    int all, all_parts, all_cuts;
-    const int at = pieces + block_scan<int>(k, &all), part = parts + block_scan<int>(k > 1 ? k : 0, &all_parts);
-    const int cut = cuts + block_scan<int>(k > 1 ? 1 : 0, &all_cuts);
+    int at[3] = {k, k > 1 ? k : 0, k > 1 ? 1 : 0}, all[3];
+    block_scan(at, all);
     for (int j = 0; j < k; ++j) {
       const long long from = (j0 + j) * each, to = from + each;
       s.v0 = j ? static_cast<int>(from - p0) : 0;
       s.v1 = j + 1 < k ? static_cast<int>(to - p0) : n;
-      s.part = k > 1 ? part + j : -1;
-      a.piece[at + j] = s;
-      if (from >= p0) a.first[j0 + j] = at + j;
+      s.part = k > 1 ? parts + at[1] + j : -1;
+      a.piece[pieces + at[0] + j] = s;
+      if (from >= p0) a.first[j0 + j] = pieces + at[0] + j;
     }
-    if (k > 1) a.cut[cut] = Cut{s.first, s.T, s.tile, part, k};
-    before += all_sizes;
-    pieces += all;
-    parts += all_parts;
-    cuts += all_cuts;
+    if (k > 1) a.cut[cuts + at[2]] = Cut{s.first, s.T, s.tile, parts + at[1], k};
+    pieces += all[0];
+    parts += all[1];
+    cuts += all[2];
   }
   if (tid == 0) {
-    const int groups = static_cast<int>((before + each - 1) / each);
-    a.first[groups] = pieces;
+    const int groups = whole ? tiles : static_cast<int>((pages + each - 1) / each);
+    a.first[groups] = whole ? tiles : pieces;
     a.counts[0] = groups;
     a.counts[1] = cuts;
   }
