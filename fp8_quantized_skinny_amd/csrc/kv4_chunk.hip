@@ -528,6 +528,7 @@ __device__ __forceinline__ void attend_piece(const ChunkArgs& a, int h, int at, 
   constexpr bool kWaits = D == 256;
   constexpr int kValueProducts = 2 * kGroup * DB, kProducts = kValueProducts + kGroup * kSteps, kAhead = D == 256 ? 3 : 6;
   constexpr int kPieces = D / 64 + D / 32;  // of a thread's widening: keys and values
+  constexpr int kDeep = kWaits ? 1 : 2;     // pages whose codes are on the way
   Tile<D>(&tiles)[2] = shared.tiles;
   auto& waiting = shared.waiting;
   auto& nan_groups = shared.nan_groups;
@@ -592,7 +593,7 @@ __device__ __forceinline__ void attend_piece(const ChunkArgs& a, int h, int at, 
   for (int d = 0; d < DB; ++d) o[d] = f32x16{};
 
   // A page that the table does not name is read as the last one and seen by nobody.
-  Raw<D> raw;
+  Raw<D> raws[kDeep];
   // The lane, found again for each page where the addresses made of it would take registers all the while.
   const auto here = [&] {
     int l = lane;
@@ -612,13 +613,13 @@ __device__ __forceinline__ void attend_piece(const ChunkArgs& a, int h, int at, 
     const uint32_t n = static_cast<uint32_t>(id);
     return blocks + static_cast<uint64_t>(page_bytes) * (n < last_page ? n : last_page);
   };
-  const auto load = [&](const uint8_t* keys, const uint8_t* values) {
+  const auto load = [&](Raw<D>& raw, int key_id, int value_id) {
     const int l = here();
     if constexpr (kWaits) {
-      waiting.load(keys, values, wave, l);
+      waiting.load(block(key_id), block(value_id), wave, l);
     } else {
-      raw.load_keys(keys, wave, l);
-      raw.load_values(values, wave, l);
+      raw.load_keys(block(key_id), wave, l);
+      raw.load_values(block(value_id), wave, l);
     }
   };
   if (half == 0) nan_groups[wave * 32 + col] = 0u;
@@ -627,24 +628,28 @@ __device__ __forceinline__ void attend_piece(const ChunkArgs& a, int h, int at, 
     if constexpr (kWaits) __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
     lds_barrier();
   };
-  int id = 0, next_id = 0, after_id = 0;  // of pages v, v + 1 and v + 2
+  int id[4] = {0, 0, 0, 0};  // of pages v .. v + 3
   if (v0 < v1) {
     // The first products are of no weights with the values of no page.
     uint32_t zero = 0u;
     asm volatile("" : "+v"(zero));
     for (int i = threadIdx.x; i < D * Tile<D>::kValueRow / 8; i += kThreads) *reinterpret_cast<u32x4*>(tiles[1].v + 8 * i) = u32x4{zero, zero, zero, zero};
-    id = page_id(v0);
-    next_id = page_id(v0 + 1);
-    after_id = page_id(v0 + 2);
-    load(block(id), block(id));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) id[i] = page_id(v0 + i);
+    load(raws[0], id[0], id[0]);
     if constexpr (kWaits) {
       arrive();
-      waiting.arrived(&raw, wave, here());
+      waiting.arrived(&raws[0], wave, here());
     }
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) widen_keys<D>(raw, key_row_of<D>(&tiles[0], wave, here()), wave, i);
+    for (int i = 0; i < D / 64; ++i) widen_keys<D>(raws[0], key_row_of<D>(&tiles[0], wave, here()), wave, i);
     if constexpr (kWaits) arrive();  // what was waiting has been read
-    load(block(next_id), block(id));
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
+      load(raws[i], id[i + 1], id[i]);
+      asm volatile("" ::: "memory");  // in this order, which the loop's waits count on
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
   arrive();
   if (wave >= kWaves / 2) lds_barrier();
@@ -680,10 +685,9 @@ __device__ __forceinline__ void attend_piece(const ChunkArgs& a, int h, int at, 
   const int easy = view.low + whole_tile.whole_begin - view.from;
   const unsigned easy_many = whole_tile.whole_end > whole_tile.whole_begin ? whole_tile.whole_end - whole_tile.whole_begin : 0;
 
-  for (int v = v0; v < v1; ++v) {
-    Tile<D>&now = tiles[(v - v0) & 1], &other = tiles[(v + 1 - v0) & 1];
-    int later_id = 0;
-    const bool whole = static_cast<unsigned>(v - easy) < easy_many && named(id);
+  // A page, whose codes are in raw.
+  const auto step = [&](int v, Raw<D>& raw, Tile<D>& now, Tile<D>& other) {
+    const bool live = named(id[0]) && (kDeep == 1 || v < v1), whole = static_cast<unsigned>(v - easy) < easy_many && live;
     bool work = busy, partial = false;
     int first = 0;
     if (flagged >= 0) add_bad(other);
@@ -697,12 +701,12 @@ __device__ __forceinline__ void attend_piece(const ChunkArgs& a, int h, int at, 
       const ChunkArgs& a = arguments();
       const Sight tile_sight(a, limits[0], limits[1]), wave_sight(a, limits[2], limits[3]);
       const int page = view.page(v);
-      const bool noted = !named(id) || !tile_sight.whole(page);
+      const bool noted = !live || !tile_sight.whole(page);
       first = page * kPage;
-      work = busy && named(id) && wave_sight.some(page);
+      work = busy && live && wave_sight.some(page);
       partial = work && !wave_sight.whole(page);
       if (noted) note_bad<D>(&raw, &now, wave, here());
-      flagged = noted && named(id) ? first : -1;
+      flagged = noted && live ? first : -1;
     }
 #pragma unroll
     for (int u0 = 0; u0 < 2; u0 += kGroup) {
@@ -758,14 +762,13 @@ __device__ __forceinline__ void attend_piece(const ChunkArgs& a, int h, int at, 
       }
       lds_barrier();
       if (u0 == 0) {
-        if (v + 3 - v_ids == 64) {
+        load(raw, id[kDeep + 1], id[kDeep]);
+        if (v + 4 - v_ids == 64) {
           v_ids += 64;
           ids = more_ids;
           more_ids = ids_of(v_ids + 64);
         }
-        later_id = page_id(v + 3);
       }
-      if (u0 == 0) load(block(after_id), block(next_id));
       if (work) {
         if (partial) {
           const ChunkArgs& a = arguments();
@@ -813,16 +816,26 @@ __device__ __forceinline__ void attend_piece(const ChunkArgs& a, int h, int at, 
       if (u0 + kGroup == 2) arrive();
       else lds_barrier();
     }
-    id = next_id;
-    next_id = after_id;
-    after_id = later_id;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) id[i] = id[i + 1];
+    id[3] = page_id(v + 4);
+  };
+  // Two pages a turn, whose registers take turns.  (Leaving the loop between them, the compiler waits for both pages'
+  // codes at the first one's use.)  An odd last turn ends with a page that nobody sees.
+  const int last_odd = kDeep == 2 ? 1 : (v1 - 1 - v0) & 1;
+  for (int v = v0; v < v1; v += kDeep) {
+    if constexpr (kDeep == 2) {
+      step(v, raws[0], tiles[0], tiles[1]);
+      step(v + 1, raws[1], tiles[1], tiles[0]);
+    } else {
+      step(v, raws[0], tiles[(v - v0) & 1], tiles[(v + 1 - v0) & 1]);
+    }
   }
   if (busy && v0 < v1) {
-    const Tile<D>& last_tile = tiles[(v1 - 1 - v0) & 1];
 #pragma unroll
-    for (int i = 0; i < kValueProducts; ++i) add_values(operand(last_tile, 2 - kGroup, last_tile, 0, i), i);
+    for (int i = 0; i < kValueProducts; ++i) add_values(operand(tiles[last_odd], 2 - kGroup, tiles[0], 0, i), i);
   }
-  if (flagged >= 0) add_bad(tiles[(v1 - 1 - v0) & 1]);
+  if (flagged >= 0) add_bad(tiles[last_odd]);
   if (wave < kWaves / 2) lds_barrier();
   store_rows<D, E>(arguments(), here(), wave, h, row0, R, tile, part, m, l, nan_groups[wave * 32 + (here() & 31)], o);
 }
