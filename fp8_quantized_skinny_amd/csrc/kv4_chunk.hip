@@ -31,6 +31,7 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kTile = 32 * kWaves;
 constexpr int kSlots = 256;  // workgroups that the CUs hold at once
 constexpr int kLeast = 16;   // fewest pages of a workgroup where tiles are cut
+constexpr int kCutPages = 24;  // what the cut tiles' parts cost a workgroup, in pages: stored by it, and read by the join
 constexpr int kPlanThreads = 256;
 constexpr int kPlanHeld = 1024;  // sequences whose rows and tiles the plan keeps in LDS
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -239,8 +240,11 @@ __global__ __launch_bounds__(kPlanThreads) void chunk_plan(const ChunkArgs a) {
     pages += all[0];
   }
   const long long slots = slots_per_head(a.c.Hk);
-  const bool whole = slots < 4 || (static_cast<long long>(tiles) >= 4 * slots && longest * 2 * slots <= pages);
   const long long even = (pages + slots - 1) / slots, each = even < kLeast ? kLeast : even;
+  // Whole tiles: in rounds of the longest, or with the longest of them last.
+  const long long rounds = (tiles + slots - 1) / slots * longest, last = even + longest / 2;
+  const bool whole = slots < 4 || (static_cast<long long>(tiles) >= 4 * slots && longest * 2 * slots <= pages) ||
+                     (rounds < last ? rounds : last) <= even + kCutPages;
   int pieces = 0, parts = 0, cuts = 0;
   long long done = 0;
   for (int i0 = 0; i0 < tiles; i0 += kPlanThreads) {
