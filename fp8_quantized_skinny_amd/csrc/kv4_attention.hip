@@ -48,17 +48,19 @@ struct AttendArgs {
   int least;     // fewest pages of a share
   float scale;
   int window, sinks;  // windowed calls: a row with limit L sees the slots from L - window on, and those below sinks
+  const int32_t* starts;  // chunks of another length for each sequence: their rows (see kv4_attention_chunk), of N
+  int N;
 };
 
-// The pages that a sequence's rows see: all up to its length, or with a window
-// the first `low`, which hold the sinks, and those from `from` on, where the
-// earliest row's window begins.
+// The pages that rows with limits from `least` to `most` see: all up to the
+// latter, or with a window the first `low`, which hold the sinks, and those from
+// `from` on, where the earliest row's window begins.
 template <bool WINDOW>
 struct View {
   int low, from, end;
-  __device__ __forceinline__ View(const AttendArgs& a, int len) : low(0), from(0), end((len + kPage - 1) / kPage) {
+  __device__ __forceinline__ View(const AttendArgs& a, int least, int most) : low(0), from(0), end((most + kPage - 1) / kPage) {
     if constexpr (WINDOW) {
-      const int least = len - (a.T - 1) - a.window;
+      least -= a.window;
       from = least > 0 ? least / kPage : 0;
       low = a.sinks / kPage + (a.sinks % kPage != 0);
       low = low < from ? low : from;
@@ -248,6 +250,27 @@ __device__ __forceinline__ void clean_values(const AttendArgs& a, VRegs<D>& v, i
       }
   }
   if (!__any(bad != 0u)) return;
+  if constexpr (WINDOW) {
+    // Row r of the sums is of the values that lanes r, 16 + r, .. hold: these rows, and no others of the query, are
+    // made NaN where it sees the token.
+    for (int rg = 0; rg < 4; ++rg)
+      for (int tg = 0; tg < 4; ++tg)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t of = __builtin_amdgcn_readlane(bad, 16 * tg + 4 * rg + e);
+          if (!of) continue;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            bool seen = false;
+            for (int i = 0; i < 16; ++i) seen |= ((of >> i) & 1u) && !hidden<true>(a, first + 16 * (i / 4) + 4 * tg + i % 4, limit[mt]);
+            if (seen && g == rg) {
+#pragma unroll
+              for (int s = 0; s < D / 16; ++s) o[mt][s][e] = NAN;
+            }
+          }
+        }
+    return;
+  }
 #pragma unroll
   for (int s = 1; s < 16; s <<= 1) bad |= __shfl_xor(bad, s);  // over the lanes of the same four tokens
 #pragma unroll
@@ -278,7 +301,7 @@ template <bool WINDOW>
 __device__ __forceinline__ Share plan_share(const AttendArgs& a, int lane) {
   const kv4_cache& c = a.c;
   const int QG = a.QG, least = a.least;
-  const auto seen = [&](int len) { return View<WINDOW>(a, len).pages(); };
+  const auto seen = [&](int len) { return View<WINDOW>(a, len - (a.T - 1), len).pages(); };
   const int per = c.Hk * QG;                      // segments of a sequence
   const int room = static_cast<int>(gridDim.x) / per;  // shares per head and query group; at least B
   const int at = static_cast<int>(blockIdx.x) / per;
@@ -338,6 +361,48 @@ __device__ __forceinline__ Share plan_share(const AttendArgs& a, int lane) {
   return s;
 }
 
+// Chunks: a workgroup has a group of `rows` rows of a head and all pages that they
+// see.  The rows of a sequence go from its start to the next one's, as in
+// kv4_chunk.hip: starts are held to 0 .. N and to what came before them.
+struct ChunkRows {
+  int T, row0;  // the sequence's tokens, and its first row
+};
+__device__ __forceinline__ Share chunk_share(const AttendArgs& a, int rows, int lane, ChunkRows* of) {
+  const int at = static_cast<int>(blockIdx.x) / a.c.Hk;
+  const auto held = [&](int s, int least) { return s < least ? least : (s > a.N ? a.N : s); };
+  Share s;
+  s.any = false;
+  s.h = static_cast<int>(blockIdx.x) % a.c.Hk;
+  s.b = s.qg = s.len = s.p0 = s.p1 = s.first = 0;
+  s.splits = 1;
+  int start = held(uniform_load(a.starts, 0), 0), before = 0;
+  for (int b0 = 0; b0 < a.c.B; b0 += 64) {
+    const int b = b0 + lane;
+    int end = held(b < a.c.B ? a.starts[b + 1] : 0, start);
+    for (int o = 1; o < 64; o <<= 1) {
+      const int x = __shfl_up(end, o);
+      if (lane >= o && x > end) end = x;
+    }
+    const int up = __shfl_up(end, 1), begin = lane ? up : start;
+    const int n = b < a.c.B ? static_cast<int>((static_cast<int64_t>(end - begin) * a.G + rows - 1) / rows) : 0;
+    const int upto = before + wave_scan(n), last = __builtin_amdgcn_readlane(upto, 63);
+    if (at < last) {
+      const int l = __popcll(__ballot(upto <= at));  // the lane of the sequence
+      s.any = true;
+      s.b = b0 + l;
+      s.qg = at - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(n, l));
+      of->row0 = __builtin_amdgcn_readlane(begin, l);
+      of->T = __builtin_amdgcn_readlane(end, l) - of->row0;
+      s.len = kv_len_uniform(a.c, __builtin_amdgcn_readfirstlane(s.b));
+      break;
+    }
+    before = last;
+    start = __builtin_amdgcn_readlane(end, 63);
+  }
+  for (int* f : {&s.b, &s.h, &s.qg, &s.len}) *f = __builtin_amdgcn_readfirstlane(*f);
+  return s;
+}
+
 // A page that the table does not name is read as page 0 and lies past every
 // limit: slots of a table are fewer than kNowhere, and kNowhere + 63 is an int.
 constexpr int kNowhere = 0x7FFFFFC0;
@@ -366,7 +431,7 @@ constexpr int attend_per_cu(int D, int MT) { return D == 256 && MT == 2 ? 1 : (D
 // VALU is busy for 59% of the cycles and the matrix unit for 29%); short
 // sequences, latency: of one sequence of 8197 tokens' 16 us a page takes 2.6
 // and the joining of four wavefronts' sums 3.
-template <int D, int MT, class E, bool WINDOW>
+template <int D, int MT, class E, bool WINDOW, bool CHUNK>
 __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const AttendArgs a) {
   constexpr int DB = D / 16;
   constexpr int kRow = D + 8;
@@ -378,17 +443,33 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
   __shared__ float stat[kWaves][MT * 16][2];
   __shared__ __align__(16) float sums[kWaves][D * 16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, c = lane & 15;
-  const Share sh = plan_share<WINDOW>(a, lane);
+  ChunkRows of{a.T, 0};
+  Share sh = CHUNK ? chunk_share(a, MT * 16, lane, &of) : plan_share<WINDOW>(a, lane);
   if (!sh.any) return;
   const int b = sh.b, h = sh.h, qg = sh.qg, len = sh.len;
-  const int R = a.T * a.G;
-  if (a.split && sh.first == static_cast<int>(blockIdx.x) && threadIdx.x == 0)
+  const int T = CHUNK ? of.T : a.T, R = T * a.G;
+  // The slots that row r sees without a window, and the least and the most of the workgroup's.
+  const auto limit_of = [&](int r) {
+    const int n = len - (T - 1 - r / a.G);
+    return CHUNK && n < 0 ? 0 : n;
+  };
+  int least = len - (T - 1), most = len;
+  kv4_rows rows = a.q;
+  if constexpr (CHUNK) {
+    const int r0 = qg * MT * 16, r1 = r0 + MT * 16 < R ? r0 + MT * 16 : R;
+    least = limit_of(r0);
+    most = limit_of(r1 - 1);
+    rows.data = static_cast<const uint16_t*>(rows.data) + of.row0 * rows.row;
+    rows.sequence = 0;
+  }
+  if (!CHUNK && a.split && sh.first == static_cast<int>(blockIdx.x) && threadIdx.x == 0)
     a.split[(b * a.c.Hk + h) * a.QG + qg] = int2{sh.first, sh.splits};
   const int32_t* table = a.c.table + static_cast<size_t>(b) * a.c.width;
-  const View<WINDOW> view(a, len);
+  const View<WINDOW> view(a, least, most);
+  if constexpr (CHUNK) sh.p1 = view.pages();
   int page = sh.p0 + wave;  // of those that the sequence's rows see
   Queries<D, MT> q;
-  q.load(a.q, b, h, qg, a.G, R);
+  q.load(rows, b, h, qg, a.G, R);
   KRegs<D> k;
   VRegs<D> v;
   Page now{nullptr, 0}, next{nullptr, 0};
@@ -402,7 +483,7 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
   q.template put<E>(qs, factor);
   if (threadIdx.x < MT * 16) {
     const int r = qg * MT * 16 + threadIdx.x;
-    limits[threadIdx.x] = r < R ? len - (a.T - 1 - r / a.G) : 0;
+    limits[threadIdx.x] = r < R ? limit_of(r) : 0;
   }
   __syncthreads();
 
@@ -448,7 +529,7 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
     }
     if constexpr (!kLateKeys) k.load(next.block, lane);
     // Some row does not see the whole page.
-    if (first > len - (a.T - 1) - kPage || (WINDOW && first < len - a.window && first + kPage > a.sinks)) {
+    if (first > least - kPage || (WINDOW && first < most - a.window && first + kPage > a.sinks)) {
       int limit[MT];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) limit[mt] = limits[mt * 16 + c];
@@ -565,7 +646,7 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
         total += f[w] * stat[w][local][1];
       }
       const int t = r / a.G;
-      const size_t at_row = (static_cast<size_t>(b) * a.T + t) * a.Hq + h * a.G + r % a.G;
+      const size_t at_row = ((CHUNK ? static_cast<size_t>(of.row0) : static_cast<size_t>(b) * a.T) + t) * a.Hq + h * a.G + r % a.G;
       const size_t at_part = (static_cast<size_t>(blockIdx.x) * MT * 16 + local);
       const float inv = sh.splits > 1 ? 1.0f : (mm == -INFINITY ? 0.0f : a.c.gv / total);
       float x[DB];
@@ -843,7 +924,7 @@ hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type,
                                 int sinks, void* out, float* lse, void* workspace, hipStream_t stream) {
   const AttendPlan p = kv4_attend_plan(c.B, T, Hq, c.Hk, c.D, c.width, window, sinks);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  AttendArgs a{c, q, out, lse, nullptr, nullptr, nullptr, T, Hq, Hq / c.Hk, p.QG, p.least, scale, window, sinks};
+  AttendArgs a{c, q, out, lse, nullptr, nullptr, nullptr, T, Hq, Hq / c.Hk, p.QG, p.least, scale, window, sinks, nullptr, 0};
   if (p.split) {
     a.part = reinterpret_cast<float*>(ws + p.part_off);
     a.stat = reinterpret_cast<float*>(ws + p.stat_off);
@@ -852,10 +933,43 @@ hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type,
   const unsigned segments = static_cast<unsigned>(c.B * c.Hk * p.QG);
   return by_shape(c.D, type, p.MT, [](int D) constexpr { return max_tiles(D); }, [&](auto d, auto mt, auto e) {
     const dim3 grid(static_cast<unsigned>(p.grid));
-    if (window) attend<d(), mt(), decltype(e), true><<<grid, kThreads, 0, stream>>>(a);
-    else attend<d(), mt(), decltype(e), false><<<grid, kThreads, 0, stream>>>(a);
+    if (window) attend<d(), mt(), decltype(e), true, false><<<grid, kThreads, 0, stream>>>(a);
+    else attend<d(), mt(), decltype(e), false, false><<<grid, kThreads, 0, stream>>>(a);
     if (p.split)
       attend_join<d(), mt(), decltype(e)><<<dim3(segments, mt() * 16), kThreads, 0, stream>>>(a);
+  });
+}
+
+// Chunks of few rows over few pages: as kv4_attention, but every workgroup has all
+// the pages of its rows, so that one launch does.  The fewest tiles of rows per
+// workgroup that leave no more workgroups than the CUs hold at once: a page takes
+// a wavefront the less.  One launch against the tiles of 256 rows of kv4_chunk.hip
+// with their plan and join (D = 128, 8 heads of 4 query heads, 9 rows; us):
+//   pages        4    16    32    64   128   256
+//   this       7.0  11.1  16.7  27.0  47.3  87.3
+//   the other 17.0  32.8  55.5  36.5  37.2  39.6
+// and 16.1, 24.5, 40.3, 72.5 against 40.7, 64.7, 65.0, 74.9 with 256 rows and 16
+// to 128 pages.  The two meet near 96 pages there and for D = 64 (29 us), and
+// between 96 and 128 for D = 256.
+SmallChunk kv4_small_chunk(int N, int B, int G, int Hk, int D, int64_t pages) {
+  constexpr int kCUs = 256, kMostPages = 96;
+  SmallChunk s{0, 0};
+  if (pages > kMostPages) return s;
+  const int64_t busy = N < B ? N : B;  // sequences with rows
+  for (int mt = 1; mt <= max_tiles(D); ++mt) {
+    const int64_t groups = (static_cast<int64_t>(N) * G + busy * (mt * 16 - 1)) / (mt * 16);
+    if (groups * Hk <= kCUs * attend_per_cu(D, mt)) return SmallChunk{mt, groups};
+  }
+  return s;
+}
+
+hipError_t launch_kv4_small_chunk(const kv4_cache& c, const void* q, int64_t row, int64_t head, const int32_t* starts, int N,
+                                  int type, int Hq, float scale, int window, int sinks, void* out, float* lse,
+                                  const SmallChunk& s, hipStream_t stream) {
+  const int wide = window ? window : c.width * kPage;  // a window that leaves nothing out
+  const AttendArgs a{c, {q, 0, row, head}, out, lse, nullptr, nullptr, nullptr, 0, Hq, Hq / c.Hk, 1, 0, scale, wide, sinks, starts, N};
+  return by_shape(c.D, type, s.tiles, [](int D) constexpr { return max_tiles(D); }, [&](auto d, auto mt, auto e) {
+    attend<d(), mt(), decltype(e), true, true><<<dim3(static_cast<unsigned>(s.groups * c.Hk)), kThreads, 0, stream>>>(a);
   });
 }
 

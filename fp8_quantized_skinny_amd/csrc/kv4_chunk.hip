@@ -900,7 +900,7 @@ size_t up(size_t n) { return (n + 255) / 256 * 256; }
 }  // namespace
 
 ChunkPlan kv4_chunk_plan(int N, int B, int Hq, int Hk, int D, int width, int window, int sinks) {
-  ChunkPlan p;
+  ChunkPlan p{};
   const int64_t G = Hq / Hk, busy = N < B ? N : B;  // sequences with rows
   p.tiles = (N * G + busy * (kTile - 1)) / kTile;
   // The pages that a tile can see: its rows' tokens, a window before the first of them, and the sinks.
@@ -909,6 +909,12 @@ ChunkPlan kv4_chunk_plan(int N, int B, int Hq, int Hk, int D, int width, int win
     const int64_t tokens = (kTile - 1) / G + 2 < N ? (kTile - 1) / G + 2 : N;
     const int64_t seen = (window + tokens) / kPage + 2 + (static_cast<int64_t>(sinks) + kPage - 1) / kPage;
     pages = seen < pages ? seen : pages;
+  }
+  p.small = kv4_small_chunk(N, B, static_cast<int>(G), Hk, D, pages);
+  if (p.small.tiles) {
+    p.groups = p.small.groups;
+    p.total = 0;
+    return p;
   }
   // Of g workgroups in a row at most g - 1 begin inside a tile, and each of these cuts makes one piece more.
   const int64_t slots = slots_per_head(Hk), even = (p.tiles * pages + kLeast - 1) / kLeast;
@@ -931,6 +937,8 @@ ChunkPlan kv4_chunk_plan(int N, int B, int Hq, int Hk, int D, int width, int win
 hipError_t launch_kv4_chunk(const kv4_cache& c, const void* q, int64_t row, int64_t head, const int32_t* starts, int N, int type,
                             int Hq, float scale, int window, int sinks, void* out, float* lse, void* workspace, hipStream_t stream) {
   const ChunkPlan p = kv4_chunk_plan(N, c.B, Hq, c.Hk, c.D, c.width, window, sinks);
+  if (p.small.tiles)
+    return launch_kv4_small_chunk(c, q, row, head, starts, N, type, Hq, scale, window, sinks, out, lse, p.small, stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const ChunkArgs a{c, static_cast<const uint16_t*>(q), row, head, starts, out, lse, reinterpret_cast<int*>(ws + p.counts_off),
                     reinterpret_cast<int*>(ws + p.begin_off), reinterpret_cast<int*>(ws + p.offset_off), reinterpret_cast<int*>(ws + p.first_off),

@@ -74,7 +74,7 @@ def kv4_attention_window(q, cache, table, lens, out, window, sinks=0, lse=None, 
 
 
 def kv4_attention_chunk_workspace_bytes(N, B, Hq, Hk, D, width, window=0, sinks=0):
-    """Workspace bytes of kv4_attention_chunk (0: an unsupported shape)."""
+    """Workspace bytes of kv4_attention_chunk (0: none needed, or an unsupported shape)."""
     return lib().kv4_attention_chunk_workspace_bytes(N, B, Hq, Hk, D, width, window, sinks)
 
 

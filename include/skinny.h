@@ -600,7 +600,7 @@ size_t kv4_attention_window_workspace_bytes(int B, int T, int Hq, int Hk, int D,
  *          slot.
  *   lse  : device fp32 [N][Hq] or NULL: -inf for a row that sees no slot.
  *   workspace : kv4_attention_chunk_workspace_bytes(...) bytes (see "Workspaces";
- *          never NULL).
+ *          may be NULL when that is 0).
  *   1 <= N, N * (Hq / Hk) < 2^31; Hq as for kv4_attention.
  * Rows before starts[0] and from starts[B] on are left as they were, in out and in
  * lse.  out may be q itself (the same pointer and strides); otherwise neither out

@@ -17,7 +17,7 @@ Q, O, W = 0x1000000, 0x2000000, 0x100000000
 
 
 def _call(c=None, q=Q, row=1024, head=128, starts=0x600000, N=20, type=0, Hq=8, scale=0.1, window=0, sinks=0, out=O, lse=0x5000000, ws=W, n=1 << 40):
-    return lib().kv4_attention_chunk(c or _cache(table=0x700000, lens=0x710000), q, row, head, starts, N, type, Hq, scale, window, sinks, out, lse, ws, n, None)
+    return lib().kv4_attention_chunk(c or _cache(table=0x700000, lens=0x710000, width=100), q, row, head, starts, N, type, Hq, scale, window, sinks, out, lse, ws, n, None)
 
 
 @pytest.mark.parametrize("bad, status", BAD_CACHES)
@@ -40,10 +40,12 @@ def test_refusals(bad, status):
 
 def test_workspaces():
     size = sk.kv4_attention_chunk_workspace_bytes
-    assert size(1, 1, 8, 4, 128, 1) > sk.WORKSPACE_SYNC_BYTES
+    # none for few rows over few pages
+    assert size(64, 3, 8, 4, 128, 96) == 0 and size(64, 3, 8, 4, 128, 97) > sk.WORKSPACE_SYNC_BYTES and size(64, 3, 8, 4, 128, 5000, 1000, 4) == 0
+    assert size(40000, 3, 8, 4, 128, 64) > sk.WORKSPACE_SYNC_BYTES
     # by the pages that can be seen, not by a wide table
-    assert size(64, 1, 8, 4, 128, 5000, 64, 4) == size(64, 1, 8, 4, 128, 100, 64, 4) < size(64, 1, 8, 4, 128, 5000)
-    assert size(64, 1, 8, 4, 128, 100, 6400, 4) == size(64, 1, 8, 4, 128, 100)
+    assert size(64, 1, 8, 4, 128, 5000, 6000, 4) == size(64, 1, 8, 4, 128, 300, 6000, 4) < size(64, 1, 8, 4, 128, 5000)
+    assert size(64, 1, 8, 4, 128, 100, 6400, 4) == size(64, 1, 8, 4, 128, 100) > 0
     for bad in ((0, 1, 8, 4, 128, 1), (1, 0, 8, 4, 128, 1), (1, 1, 7, 4, 128, 1), (1, 1, 8, 4, 96, 1), (1, 1, 8, 4, 128, 0), (1 << 30, 1, 8, 4, 128, 1),
                 (1, 1, 8, 4, 128, 1, -1), (1, 1, 8, 4, 128, 1, 5, -1)):
         assert size(*bad) == 0, bad
@@ -74,9 +76,15 @@ CHUNKS = [  # type, D, Hq, Hk, chunks, lens, window, sinks
 ]
 
 
-def _inputs(rng, kind, D, Hq, Hk, chunks, lens, pad=3, q_size=2.0):
-    """Pages as for the steps of a few rows; packed queries in a qkv GEMM's output, `pad` rows before the first and behind the last."""
+WIDE = pytest.mark.parametrize("wide", [False, True])  # few rows over few pages, and any over a table of more than 96, go different ways
+
+
+def _inputs(rng, kind, D, Hq, Hk, chunks, lens, wide, pad=3, q_size=2.0):
+    """Pages as for the steps of a few rows, a wide table with 100 columns more that name none; packed queries in a qkv
+    GEMM's output, `pad` rows before the first and behind the last."""
     table, cache, _ = _attend_inputs(rng, kind, D, Hq, Hk, 1, lens)
+    if wide:
+        table = np.concatenate([table, np.full((len(lens), 100), -1, np.int32)], 1)
     N = sum(chunks) + 2 * pad
     qkv = torch.from_numpy(rng.standard_normal((N, (Hq + 2 * Hk) * D)) * q_size).to(TYPES[kind])
     starts = pad + np.concatenate([[0], np.cumsum(chunks)]).astype(np.int32)
@@ -116,10 +124,11 @@ def _some(rng, chunks, Hq, most=300):
 
 
 @gpu
+@WIDE
 @pytest.mark.parametrize("kind, D, Hq, Hk, chunks, lens, window, sinks", CHUNKS)
-def test_chunks(kind, D, Hq, Hk, chunks, lens, window, sinks):
+def test_chunks(kind, D, Hq, Hk, chunks, lens, window, sinks, wide):
     rng = np.random.default_rng(D + Hq + sum(chunks) + window)
-    table, cache, qkv, starts = _inputs(rng, kind, D, Hq, Hk, chunks, lens)
+    table, cache, qkv, starts = _inputs(rng, kind, D, Hq, Hk, chunks, lens, wide)
     B, width = table.shape
     for b, n in enumerate(lens):  # pages that no row sees: NaN and pages that are none
         for p in range(-(-sinks // 64), max(0, n - chunks[b] + 1 - window) // 64 if window and chunks[b] else 0):
@@ -134,7 +143,8 @@ def test_chunks(kind, D, Hq, Hk, chunks, lens, window, sinks):
     more = dict(scale=scale, window=window, sinks=sinks, gk=gk, gv=gv, workspace=ws)
     for _ in range(2):  # a workspace serves again
         sk.kv4_attention_chunk(q, *args, out, lse=lse, **more)
-    assert (ws[:sk.WORKSPACE_SYNC_BYTES] == 0).all()
+    assert ws is None or (ws[:sk.WORKSPACE_SYNC_BYTES] == 0).all()
+    assert ws is not None or not wide or window
     for t in (out, lse):  # rows that no sequence has
         assert (t[:starts[0]] == 3).all() and (t[starts[-1]:] == 3).all()
     again = torch.full_like(out, 4.0)
@@ -148,11 +158,12 @@ def test_chunks(kind, D, Hq, Hk, chunks, lens, window, sinks):
 
 
 @gpu
-def test_a_prompt_agrees_with_its_last_rows_one_by_one():
+@WIDE
+def test_a_prompt_agrees_with_its_last_rows_one_by_one(wide):
     """A long prompt's rows against kv4_attention of the same rows, eight at a time."""
     rng = np.random.default_rng(2)
     D, Hq, Hk, n = 128, 16, 2, 1500
-    table, cache, qkv, starts = _inputs(rng, "bf16", D, Hq, Hk, [n], [n], pad=0)
+    table, cache, qkv, starts = _inputs(rng, "bf16", D, Hq, Hk, [n], [n], wide, pad=0)
     q = qkv.cuda()[:, :Hq * D].unflatten(-1, (Hq, D))
     c, t = _cuda(cache), _cuda(table)
     out, lse = torch.empty((n, Hq, D), dtype=torch.bfloat16, device="cuda"), torch.empty((n, Hq), device="cuda")
@@ -168,10 +179,11 @@ def test_a_prompt_agrees_with_its_last_rows_one_by_one():
 
 
 @gpu
-def test_a_missing_page_is_skipped():
+@WIDE
+def test_a_missing_page_is_skipped(wide):
     rng = np.random.default_rng(5)
     chunks, lens, D, Hq, Hk = [100, 30], [200, 2000], 128, 8, 2
-    table, cache, qkv, starts = _inputs(rng, "f16", D, Hq, Hk, chunks, lens)
+    table, cache, qkv, starts = _inputs(rng, "f16", D, Hq, Hk, chunks, lens, wide)
     table[0, 1], table[0, 3], table[1, 0], table[1, 7:20] = -1, 2 ** 31 - 1, len(cache), -7
     q = qkv.cuda()[:, :Hq * D].unflatten(-1, (Hq, D))
     out, lse = torch.empty(q.shape, dtype=torch.float16, device="cuda"), torch.empty(q.shape[:2], device="cuda")
@@ -181,12 +193,13 @@ def test_a_missing_page_is_skipped():
 
 
 @gpu
+@WIDE
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("window, sinks", [(0, 0), (40, 3)])
-def test_a_nan_value_reaches_only_the_rows_that_see_it(D, window, sinks):
+def test_a_nan_value_reaches_only_the_rows_that_see_it(D, window, sinks, wide):
     rng = np.random.default_rng(6)
     chunks, lens, Hq, Hk = [70], [200], 12, 2
-    table, cache, qkv, starts = _inputs(rng, "f16", D, Hq, Hk, chunks, lens)
+    table, cache, qkv, starts = _inputs(rng, "f16", D, Hq, Hk, chunks, lens, wide)
     places = oracle.kv_places(D)
     for s, at in ((150, places[4][150 % 64, D - 16]), (2, places[4][2, 0]), (133, places[4][133 % 64, 16])):
         cache[table[0, s // 64], :, at] = 0x7F
@@ -210,11 +223,12 @@ def test_a_nan_value_reaches_only_the_rows_that_see_it(D, window, sinks):
 
 
 @gpu
-def test_starts_that_fall_or_leave_the_rows():
+@WIDE
+def test_starts_that_fall_or_leave_the_rows(wide):
     """Rows never belong to two sequences, and none outside q is touched."""
     rng = np.random.default_rng(7)
     D, Hq, Hk, N, lens = 64, 4, 2, 50, [70, 80, 90, 100]
-    table, cache, qkv, _ = _inputs(rng, "f16", D, Hq, Hk, [N], lens, pad=0)
+    table, cache, qkv, _ = _inputs(rng, "f16", D, Hq, Hk, [N], lens, wide, pad=0)
     q = qkv.cuda()[:, :Hq * D].unflatten(-1, (Hq, D))
     args = (_cuda(cache), _cuda(table), _cuda(np.array(lens, np.int32)))
     ws = sk.new_workspace(sk.kv4_attention_chunk_workspace_bytes(N, 4, Hq, Hk, D, table.shape[1]))
@@ -231,15 +245,18 @@ def test_starts_that_fall_or_leave_the_rows():
 
 
 @gpu
-def test_lens_beyond_the_table_and_below_zero_are_clamped():
+@WIDE
+def test_lens_beyond_the_table_and_below_zero_are_clamped(wide):
     rng = np.random.default_rng(9)
     D, Hk, Hq = 64, 1, 4
-    table, cache, qkv, starts = _inputs(rng, "f16", D, Hq, Hk, [20, 20], [128, 100], pad=0)
-    table = table[:, :2].copy()
+    table, cache, qkv, starts = _inputs(rng, "f16", D, Hq, Hk, [20, 20], [128, 100], False, pad=0)
+    table = np.repeat(table[:, :2], 50 if wide else 1, 1)  # (pages may be named twice)
+    n = 64 * table.shape[1]
     q = qkv.cuda()[:, :Hq * D].unflatten(-1, (Hq, D))
-    ws = sk.new_workspace(sk.kv4_attention_chunk_workspace_bytes(40, 2, Hq, Hk, D, 2))
+    ws = sk.new_workspace(sk.kv4_attention_chunk_workspace_bytes(40, 2, Hq, Hk, D, table.shape[1]))
+    assert (ws is not None) == wide
     got = []
-    for lens in ([1000, -5], [128, 0]):
+    for lens in ([n + 1000, -5], [n, 0]):
         out, lse = torch.empty(q.shape, dtype=torch.float16, device="cuda"), torch.empty(q.shape[:2], device="cuda")
         sk.kv4_attention_chunk(q, _cuda(starts), _cuda(cache), _cuda(table), _cuda(np.array(lens, np.int32)), out, lse=lse, workspace=ws)
         got.append((out, lse))
@@ -249,12 +266,13 @@ def test_lens_beyond_the_table_and_below_zero_are_clamped():
 
 
 @gpu
+@WIDE
 @pytest.mark.parametrize("kind, size", [("f16", 3e4), ("bf16", 1e30), ("bf16", 1e-30), ("f16", 1e-7)])
-def test_queries_of_extreme_size(kind, size):
+def test_queries_of_extreme_size(kind, size, wide):
     """Scores far beyond the usual: one slot takes all, or all the same."""
     rng = np.random.default_rng(7)
     chunks, lens, D, Hq, Hk = [40], [150], 128, 4, 1
-    table, cache, qkv, starts = _inputs(rng, kind, D, Hq, Hk, chunks, lens, q_size=size)
+    table, cache, qkv, starts = _inputs(rng, kind, D, Hq, Hk, chunks, lens, wide, q_size=size)
     qkv[5, :D] = 0.0
     q = qkv.cuda()[:, :Hq * D].unflatten(-1, (Hq, D))
     q.clamp_(-6e4, 6e4) if kind == "f16" else None  # infinite queries are tested by themselves
@@ -266,10 +284,11 @@ def test_queries_of_extreme_size(kind, size):
 
 
 @gpu
-def test_infinite_and_nan_queries_stay_in_their_rows():
+@WIDE
+def test_infinite_and_nan_queries_stay_in_their_rows(wide):
     rng = np.random.default_rng(8)
     chunks, lens, D, Hq, Hk = [40], [150], 64, 2, 1
-    table, cache, qkv, starts = _inputs(rng, "f16", D, Hq, Hk, chunks, lens)
+    table, cache, qkv, starts = _inputs(rng, "f16", D, Hq, Hk, chunks, lens, wide)
     clean = qkv.clone()
     qkv[10, 3], qkv[20, 5] = float("inf"), float("nan")
     got = []
@@ -286,23 +305,26 @@ def test_infinite_and_nan_queries_stay_in_their_rows():
 
 
 @gpu
-def test_offsets_past_32_bits():
+@WIDE
+def test_offsets_past_32_bits(wide):
     D, Hk, Hq, T, n = 128, 2, 8, 30, 190
     pages = (1 << 32) // (Hk * 72 * D) + 64
     rng = np.random.default_rng(8)
-    table, small, qkv, starts = _inputs(rng, "f16", D, Hq, Hk, [T], [n], pad=0)
-    small, table = small[:4], np.arange(4, dtype=np.int32)[None]
+    table, small, qkv, starts = _inputs(rng, "f16", D, Hq, Hk, [T], [n], wide, pad=0)
+    small, none = small[:4], np.full((1, table.shape[1] - 4 if wide else 0), -1, np.int32)
+    table = np.concatenate([np.arange(4, dtype=np.int32)[None], none], 1)
     cache = torch.empty((pages, Hk, 72 * D), dtype=torch.uint8, device="cuda")
     ids = np.array([[pages - 1, pages - 9, pages - 2, pages - 40]], np.int32)
     for i, p in enumerate(ids[0]):
         cache[p] = _cuda(small[i])
+    ids = np.concatenate([ids, none], 1)
     # Rows far apart: the last of a view whose elements span more than 2^32 bytes.
     far = torch.empty((T, (1 << 32) // (2 * (T - 1)) // 8 * 8 + 4096), dtype=torch.float16, device="cuda")
     far[:, :Hq * D] = qkv.cuda()[:, :Hq * D]
     got = []
     for q, c, t in ((far, cache, ids), (qkv.cuda(), _cuda(small), table)):
         out, lse = torch.empty((T, Hq, D), dtype=torch.float16, device="cuda"), torch.empty((T, Hq), device="cuda")
-        ws = sk.new_workspace(sk.kv4_attention_chunk_workspace_bytes(T, 1, Hq, Hk, D, 4))
+        ws = sk.new_workspace(sk.kv4_attention_chunk_workspace_bytes(T, 1, Hq, Hk, D, t.shape[1]))
         sk.kv4_attention_chunk(q[:, :Hq * D].unflatten(-1, (Hq, D)), _cuda(starts), c, _cuda(t), _cuda(np.array([n], np.int32)), out, lse=lse, workspace=ws)
         got.append((out, lse))
     for a, b in zip(*got):
@@ -310,11 +332,12 @@ def test_offsets_past_32_bits():
 
 
 @gpu
-def test_two_calls_at_once_and_replays_of_a_graph():
+@WIDE
+def test_two_calls_at_once_and_replays_of_a_graph(wide):
     """Two streams with a workspace each; a captured call whose starts and lengths change between the replays."""
     rng = np.random.default_rng(10)
     D, Hk, Hq, chunks, lens = 128, 4, 48, [60, 1, 25], [900, 2130, 64]
-    table, cache, qkv, starts = _inputs(rng, "bf16", D, Hq, Hk, chunks, lens)
+    table, cache, qkv, starts = _inputs(rng, "bf16", D, Hq, Hk, chunks, lens, wide)
     B, width = table.shape
     N, dev = len(qkv), qkv.cuda()
     q = dev[:, :Hq * D].unflatten(-1, (Hq, D))
@@ -352,9 +375,9 @@ def test_two_calls_at_once_and_replays_of_a_graph():
 def test_binding_refuses_what_does_not_fit():
     D, Hq, Hk = 64, 4, 2
     q, cache = torch.zeros((6, Hq, D), dtype=torch.float16, device="cuda"), torch.zeros((4, Hk, 72 * D), dtype=torch.uint8, device="cuda")
-    table, lens, starts = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([[0, 1], [2, 3]], [3, 3], [0, 3, 6]))
+    table, lens, starts = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([[0, 1] * 60, [2, 3] * 60], [3, 3], [0, 3, 6]))
     good = dict(q=q, starts=starts, cache=cache, table=table, lens=lens, out=torch.empty_like(q), lse=torch.empty((6, Hq), device="cuda"),
-                workspace=sk.new_workspace(sk.kv4_attention_chunk_workspace_bytes(6, 2, Hq, Hk, D, 2)))
+                workspace=sk.new_workspace(sk.kv4_attention_chunk_workspace_bytes(6, 2, Hq, Hk, D, 120)))
     sk.kv4_attention_chunk(**good)
     for name, value, error in (("q", q.float(), (TypeError, sk.SkinnyError)), ("q", q[None], TypeError), ("q", q[:, :, :32], ValueError), ("q", q[:0], ValueError),
                                ("starts", starts[:2], ValueError), ("starts", starts.long(), TypeError), ("out", good["out"][:5], ValueError),
