@@ -891,6 +891,9 @@ hipError_t by_shape(int D, int type, int tiles, M most, F f) {
 //
 // With a window a sequence's rows see at most the pages of window + T - 1 slots in
 // a row and those of the sinks, and the plan goes by these instead of the width.
+// A call that is split has a page per wavefront then: one sequence, a window of
+// 1024, 10.4 us with five shares a head, 11.6 with two, 12.9 in one launch; 48
+// sequences within 4096, 29.6 either way.
 AttendPlan kv4_attend_plan(int B, int T, int Hq, int Hk, int D, int width, int window, int sinks) {
   AttendPlan p;
   if (window) {
@@ -904,6 +907,7 @@ AttendPlan kv4_attend_plan(int B, int T, int Hq, int Hk, int D, int width, int w
   p.least = p.MT == 1 ? 2 * kWaves : kWaves;
   const int64_t segments = static_cast<int64_t>(B) * Hk * p.QG;
   p.split = width > p.least;
+  if (window) p.least = kWaves;
   int64_t grid = segments;
   if (p.split) {
     grid = kCUs * attend_per_cu(D, p.MT);

@@ -10,6 +10,11 @@
 // mean is a sum over neighbouring lanes and the other half of a pair lies in
 // the lane itself or rot / 16 lanes away.  The lanes find the token's angles
 // together, one or two each, while the heads arrive.
+//
+// Few tokens are bound by latency (one token, 48 + 4 heads of 128: 2.8 us, four
+// loads one behind the other between launch and store), many by memory: 32768
+// tokens of these heads, 0.87 GB read and written, 187 us at the 4.68 TB/s of a
+// large copy and 174 to 205 here.
 #include <hip/hip_runtime.h>
 
 #include "kv4.cuh"
@@ -157,9 +162,20 @@ int64_t rope_groups(int tokens, int Hq, int Hk, int D) {
   return (static_cast<int64_t>(tokens) * ((Hq + heads - 1) / heads + (Hk + heads - 1) / heads) + kWaves - 1) / kWaves;
 }
 
+// Four groups of heads per wavefront, which find the angles and weights once, where
+// the query heads fill them and there are wavefronts for the CUs even so.  One
+// against four groups (us):
+//   tokens                          1     64    256    512   1024   4096
+//   48 + 4 heads of 128, one     2.81   3.04   4.21   5.83   8.85   28.1
+//                        four    3.79   4.04   4.40   5.41   7.90   26.1
+//   24 + 4 heads of 256, one     2.99   3.27   4.54   6.41   10.2   32.8
+//                        four    3.99   4.37   4.74   5.79   8.60   28.2
+//   8 + 1 heads of 128, one      2.58   2.94   2.98   3.16   3.70   8.12
+//   (two groups)         four    3.25   3.71   3.78   3.84   4.43   9.83
 hipError_t launch_norm_rope(const RopeArgs& a, int type, int D, bool interleaved, hipStream_t stream) {
+  const bool fills = a.Hq * D > 3 * 512;  // four groups of query heads at least
   const auto run = [&](auto d, auto e) {
-    if (rope_groups(a.tokens, a.Hq, a.Hk, D) < 1024) launch<d(), decltype(e), 1>(a, interleaved, stream);
+    if (!fills || rope_groups(a.tokens, a.Hq, a.Hk, D) < 1024) launch<d(), decltype(e), 1>(a, interleaved, stream);
     else launch<d(), decltype(e), 4>(a, interleaved, stream);
   };
   const auto by_type = [&](auto d) {

@@ -85,6 +85,8 @@ CASES = [  # type, B, T, Hq, Hk, D, rot, interleaved, norm, amplitude, greatest 
     ("bf16", 1, 4, 8, 2, 128, 0, False, True, 1.0, 10),
     ("f16", 1, 4, 8, 2, 64, 0, True, False, 3.0, 10),
     ("f16", 5, 200, 24, 4, 256, 32, False, False, 1.0, 50000),
+    ("f16", 1, 900, 27, 5, 64, 64, False, True, 1.0, 50000),
+    ("bf16", 1, 1400, 8, 1, 128, 64, False, True, 1.0, 50000),
 ]
 
 
