@@ -487,13 +487,14 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
   }
   __syncthreads();
 
-  float cm[MT], m[MT], l[MT];
+  float cm[MT], m[MT], l[MT], l_over[MT];  // l_over: what rounding put into l beyond the weights' sum (windows)
   f32x4 o[MT][DB];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     cm[mt] = fmaxf(a.scale * a.c.gk * kLog2e * factor[mt * 16 + c], kMinNormal);
     m[mt] = -INFINITY;
     l[mt] = 0.0f;
+    l_over[mt] = 0.0f;
 #pragma unroll
     for (int s = 0; s < DB; ++s) o[mt][s] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
@@ -562,6 +563,7 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
         const float alpha = up ? __builtin_amdgcn_exp2f(m[mt] - to) : 1.0f;
         m[mt] = to;
         l[mt] *= alpha;
+        if constexpr (WINDOW) l_over[mt] *= alpha;
 #pragma unroll
         for (int d = 0; d < DB; ++d) o[mt][d] *= alpha;
       }
@@ -570,14 +572,23 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       const float lifted = m[mt] == -INFINITY ? 0.0f : m[mt] - kLift;
+      float sum = WINDOW ? 0.0f : l[mt];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][mt][e], cm[mt], -lifted));
-          l[mt] += w;
+          sum += w;
           p[j / 2][mt][(j % 2) * 4 + e] = static_cast<_Float16>(w);
         }
+      if constexpr (WINDOW) {  // what an addition loses goes into the next one, as in kv4_chunk.hip
+        sum -= l_over[mt];
+        const float more = l[mt] + sum;
+        l_over[mt] = (more - l[mt]) - sum;
+        l[mt] = more;
+      } else {
+        l[mt] = sum;
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (kLateKeys) k.load(next.block, lane);

@@ -591,7 +591,7 @@ __device__ __forceinline__ void attend_piece(const ChunkArgs& a, int h, int at, 
     // The loop must not wait for these again, and with them for the next page.
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
   }
-  float m = -INFINITY, l = 0.0f;
+  float m = -INFINITY, l = 0.0f, l_over = 0.0f;  // l_over: what rounding put into l beyond the weights' sum
   f32x16 o[DB];
 #pragma unroll
   for (int d = 0; d < DB; ++d) o[d] = f32x16{};
@@ -801,18 +801,26 @@ __device__ __forceinline__ void attend_piece(const ChunkArgs& a, int h, int at, 
           const float alpha = up ? __builtin_amdgcn_exp2f(m - to) : 1.0f;
           m = to;
           l *= alpha;
+          l_over *= alpha;
 #pragma unroll
           for (int d = 0; d < DB; ++d) o[d] *= alpha;
         }
         const float lifted = m == -INFINITY ? 0.0f : m - kLift;
+        float sum = 0.0f;
 #pragma unroll
         for (int u = 0; u < kGroup; ++u)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][e], cm, -lifted));
-            l += x;
+            sum += x;
             w[2 * u + e / 8][e % 8] = static_cast<_Float16>(x);
           }
+        // A long sequence's slots may each be too small for a sum of thousands of pages (120000 slots: the log-sum was off
+        // by 1e-4): what an addition loses goes into the next one.
+        sum -= l_over;
+        const float more = l + sum;
+        l_over = (more - l) - sum;
+        l = more;
       } else {
 #pragma unroll
         for (int i = 0; i < 2 * kGroup; ++i) w[i] = f16x8{};

@@ -386,3 +386,44 @@ def test_binding_refuses_what_does_not_fit():
                                ("q", q.transpose(1, 2), ValueError)):
         with pytest.raises(error):
             sk.kv4_attention_chunk(**{**good, name: value})
+
+
+@gpu
+@pytest.mark.parametrize("D, call", [(64, "chunk"), (128, "chunk"), (256, "chunk"), (64, "window"), (128, "window"), (256, "window")])
+def test_many_slots_of_little_weight_count(D, call):
+    """One slot in front, and so many of 2^-25.5 of its weight that together they are more than the tolerance: no sum over
+    pages may lose them.  Rows and sequences enough that a workgroup has thousands of pages; every fourth page is another."""
+    Hk, Hq, pages = 1, 2, 4000
+    n = 64 * pages
+    cache = np.zeros((3, Hk, 72 * D), np.uint8)
+    one, none = np.full(D, 2, np.uint8), np.zeros(D, np.uint8)  # codes of 1.0 and 0
+    some = np.where(np.arange(D) < D // 8, 2, 1).astype(np.uint8)  # 1.0, and 0.5 from D / 8 on
+    unit = np.full(D // 16, 0x38, np.uint8)  # scales of 1.0
+    for t in range(64):
+        for p, code in enumerate((one if t == 0 else none, some, none)):
+            oracle.kv_put(cache[p, 0], t, code, unit, one, unit)
+    ids = np.array([0] + [2 if p % 4 == 0 else 1 for p in range(1, pages)], np.int32)
+    # The first slot's score is x, most others' 9 x / 16, the rest's 0: the second is at e^-17.7 of the first's weight.
+    value = float(torch.tensor(17.7 * 16 / 7 / D).bfloat16())
+    x = value * D
+    lens = np.array([n], np.int32)
+    if call == "chunk":
+        T = 32768
+        q = torch.full((T, Hq, D), value, dtype=torch.bfloat16, device="cuda")
+        out, lse = torch.empty_like(q), torch.empty((T, Hq), device="cuda")
+        ws = sk.new_workspace(sk.kv4_attention_chunk_workspace_bytes(T, 1, Hq, Hk, D, pages))
+        sk.kv4_attention_chunk(q, _cuda(np.array([0, T], np.int32)), _cuda(cache), _cuda(ids[None]), _cuda(lens), out, lse=lse, scale=1.0, workspace=ws)
+        limits = n - T + 1 + np.arange(T)
+    else:
+        B = 512
+        q = torch.full((B, 1, Hq, D), value, dtype=torch.bfloat16, device="cuda")
+        out, lse = torch.empty_like(q), torch.empty((B, 1, Hq), device="cuda")
+        ws = sk.new_workspace(sk.kv4_attention_window_workspace_bytes(B, 1, Hq, Hk, D, pages, n))
+        sk.kv4_attention_window(q, _cuda(cache), _cuda(ids[None].repeat(B, 0)), _cuda(lens.repeat(B)), out, n, lse=lse, scale=1.0, workspace=ws)
+        limits = np.full(B, n)
+    light = np.concatenate([[0], np.cumsum(np.repeat(ids == 1, 64))])[limits]
+    want = x + np.log1p(light * np.exp(-x * 7 / 16) + (limits - 1 - light) * np.exp(-x))
+    assert (want - x > 2.0 ** -9).all()
+    # a score's fp32 roundings, the exponential's of numbers up to 64, and the log-sum's own: 2^-24 of 64 each, sixteen of them
+    assert (np.abs(lse.double().cpu().numpy().reshape(len(limits), Hq) - want[:, None]) <= 16 * 64 * 2.0 ** -24).all()
+    assert (out.double() - 1.0).abs().max().item() <= 2.0 ** -8
