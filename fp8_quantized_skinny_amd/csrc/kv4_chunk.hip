@@ -32,6 +32,7 @@ constexpr int kTile = 32 * kWaves;
 constexpr int kSlots = 256;  // workgroups that the CUs hold at once
 constexpr int kLeast = 16;   // fewest pages of a workgroup where tiles are cut
 constexpr int kCutPages = 24;  // what the cut tiles' parts cost a workgroup, in pages: stored by it, and read by the join
+constexpr int kBegin = 10;     // what a tile's beginning and end cost, in pages (less than kLeast; see the plan)
 constexpr int kPlanThreads = 256;
 constexpr int kPlanHeld = 1024;  // sequences whose rows and tiles the plan keeps in LDS
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -67,7 +68,7 @@ struct ChunkArgs {
   Piece* piece;
   Cut* cut;
   float* stat;          // [head][part][kTile][2]: reference maximum (log2) and sum
-  float* part;          // [head][part][kTile][D]
+  float* part;          // [head][part][kTile * D] (see part_at)
   int64_t parts;        // per head
   int N, Hq, G;
   int window, sinks;
@@ -126,7 +127,11 @@ struct Sight {
 // all tiles in a row are dealt out evenly to as many workgroups as the CUs hold:
 // each has the end of one tile, whole ones, and the beginning of another, and no
 // CU waits for a last long tile (512 tokens over 120000, 24 tiles of 1883 pages a
-// head: 1754 us with each tile in six equal shares, TODO so).
+// head: 1754 us with each tile in six equal shares, 1442 so).  A tile counts kBegin
+// pages more than it has, or the workgroup with the shortest tiles, up to eleven of
+// them, ends last: 16 chunks of 1 .. 640 tokens over up to 9000, five draws, took
+// 514, 369, 424, 419 and 344 us with 0, 476, 343, 362, 362 and 283 with 5, 468, 338,
+// 359, 336 and 260 with 10, and 470, 341, 355, 334 and 262 with 14.
 //
 // The rows of a sequence go from its start to the next one's; a start that is not
 // in 0 .. N counts as the nearer of these, and one below an earlier start as that:
@@ -223,7 +228,7 @@ __global__ __launch_bounds__(kPlanThreads) void chunk_plan(const ChunkArgs a) {
     s->tile = tiles_of(s->T) - 1 - (i - (held ? held_offset[lo] : a.offset[lo]));
     return view_of(a, held ? held_len[lo] : kv_len(a.c, lo), s->T, s->tile).pages();
   };
-  // A tile whose rows see nothing counts as one page.
+  // A tile whose rows see nothing counts as one page; its beginning and end as kBegin, before its pages.
   Piece s{};
   long long pages = 0, before[1] = {0};  // of all tiles; of those before the thread's last
   int longest = 0, n = 0;
@@ -234,7 +239,7 @@ __global__ __launch_bounds__(kPlanThreads) void chunk_plan(const ChunkArgs a) {
     block_running_max(n, &top);
     longest = top > longest ? top : longest;
     long long all[1];
-    before[0] = i < tiles ? (n ? n : 1) : 0;
+    before[0] = i < tiles ? (n ? n : 1) + kBegin : 0;
     block_scan(before, all);
     before[0] += pages;
     pages += all[0];
@@ -242,7 +247,7 @@ __global__ __launch_bounds__(kPlanThreads) void chunk_plan(const ChunkArgs a) {
   const long long slots = slots_per_head(a.c.Hk);
   const long long even = (pages + slots - 1) / slots, each = even < kLeast ? kLeast : even;
   // Whole tiles: in rounds of the longest, or with the longest of them last.
-  const long long rounds = (tiles + slots - 1) / slots * longest, last = even + longest / 2;
+  const long long rounds = (tiles + slots - 1) / slots * (longest + kBegin), last = even + longest / 2;
   const bool whole = slots < 4 || (static_cast<long long>(tiles) >= 4 * slots && longest * 2 * slots <= pages) ||
                      (rounds < last ? rounds : last) <= even + kCutPages;
   int pieces = 0, parts = 0, cuts = 0;
@@ -262,12 +267,12 @@ __global__ __launch_bounds__(kPlanThreads) void chunk_plan(const ChunkArgs a) {
     if (tiles > kPlanThreads) {  // otherwise known from before
       n = i < tiles ? find(i, &s) : 0;
       long long all[1];
-      before[0] = i < tiles ? (n ? n : 1) : 0;
+      before[0] = i < tiles ? (n ? n : 1) + kBegin : 0;
       block_scan(before, all);
       before[0] += done;
       done += all[0];
     }
-    const long long p0 = before[0], p1 = p0 + (n ? n : 1);
+    const long long p0 = before[0] + kBegin, p1 = p0 + (n ? n : 1);  // its pages in the row of all
     // Its workgroups; in 32 bits wherever the pages are counted in those, which a division takes a tenth of the time for.
     const bool few = pages <= 0x7FFFFFFF;
     const long long j0 = few ? static_cast<uint32_t>(p0) / static_cast<uint32_t>(each) : p0 / each;
@@ -281,7 +286,7 @@ __global__ __launch_bounds__(kPlanThreads) void chunk_plan(const ChunkArgs a) {
       s.v1 = j + 1 < k ? static_cast<int>(to - p0) : n;
       s.part = k > 1 ? parts + at[1] + j : -1;
       a.piece[pieces + at[0] + j] = s;
-      if (from >= p0) a.first[j0 + j] = pieces + at[0] + j;
+      if (from >= before[0]) a.first[j0 + j] = pieces + at[0] + j;
     }
     if (k > 1) a.cut[cuts + at[2]] = Cut{s.first, s.T, s.tile, parts + at[1], k};
     pieces += all[0];
@@ -470,43 +475,63 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// A wavefront's rows, or its part of them where the tile is split.
+// Where the parts of a cut tile lie: as the wavefronts hold them, so that 64 lanes store and load 1024 bytes in a row.
+// Unit wave * 8 + i: the wavefront's lanes have row lane % 32, positions c * D/16 .. for c = first_position(i, lane / 32).
+__device__ __forceinline__ int first_position(int i, int half) { return 8 * (i / 4) + 4 * half + i % 4; }
+template <int D>
+__device__ __forceinline__ size_t part_at(size_t part, int unit, int quarter, int lane) {
+  return part * (kTile * D) + static_cast<size_t>(((unit * (D / 64) + quarter) * 64 + lane) * 4);
+}
+template <int D>
+constexpr int kStageRow = 2 * D + 16;  // bytes: rows are 16 off the banks' period
+
+// A wavefront's rows, or its part of them where the tile is split.  Whole rows go through LDS to be stored 1024 bytes at
+// a time; from the lanes' own positions every store meets 32 rows, and a tile's took as long as four of its pages.
 template <int D, class E>
 __device__ __forceinline__ void store_rows(const ChunkArgs& a, int lane, int wave, int h, int row0, int R, int tile, int part, float m, float l,
-                                           uint32_t nan_groups, f32x16 (&o)[D / 32]) {
+                                           uint32_t nan_groups, f32x16 (&o)[D / 32], uint8_t* stage) {
   const int half = lane >> 5, local = wave * 32 + (lane & 31), r = tile * kTile + local;
   const float total = sum_over_halves(l);
   const float inv = part >= 0 ? 1.0f : (m == -INFINITY ? 0.0f : a.c.gv / total);
-  if (r >= R) return;
-  const size_t at_part = (static_cast<size_t>(h) * a.parts + part) * kTile + local;
-  const size_t at_row = static_cast<size_t>(row0 + r / a.G) * a.Hq + h * a.G + r % a.G;
+  const size_t at_part = static_cast<size_t>(h) * a.parts + part;
 #pragma unroll
-  for (int g = 0; g < 2; ++g)
+  for (int i = 0; i < 8; ++i) {
+    const int c = first_position(i, half);
+    float x[D / 16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // Positions c * D/16 .. of this lane.
-      const int c = 8 * g + 4 * half + i;
-      float x[D / 16];
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) x[j] = (nan_groups >> (c * D / 256)) & 1u ? NAN : o[j / 2][8 * (j % 2) + 4 * g + i] * inv;
-      if (part >= 0) {
-#pragma unroll
-        for (int j = 0; j < D / 16; j += 4)
-          *reinterpret_cast<f32x4*>(a.part + at_part * D + c * (D / 16) + j) = f32x4{x[j], x[j + 1], x[j + 2], x[j + 3]};
-      } else {
-        uint16_t* dst = static_cast<uint16_t*>(a.out) + at_row * D + c * (D / 16);
-#pragma unroll
-        for (int j = 0; j < D / 16; j += 4)
-          *reinterpret_cast<u32x2*>(dst + j) = u32x2{elem_pack<E>(x[j], x[j + 1]), elem_pack<E>(x[j + 2], x[j + 3])};
-      }
-    }
-  if (half == 0) {
+    for (int j = 0; j < D / 16; ++j) x[j] = (nan_groups >> (c * D / 256)) & 1u ? NAN : o[j / 2][8 * (j % 2) + i] * inv;
     if (part >= 0) {
-      a.stat[at_part * 2] = m;
-      a.stat[at_part * 2 + 1] = total;
+      if (r < R) {
+#pragma unroll
+        for (int j = 0; j < D / 16; j += 4)
+          *reinterpret_cast<f32x4*>(a.part + part_at<D>(at_part, wave * 8 + i, j / 4, lane)) = f32x4{x[j], x[j + 1], x[j + 2], x[j + 3]};
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < D / 16; j += 4)
+        *reinterpret_cast<u32x2*>(stage + (lane & 31) * kStageRow<D> + c * (D / 8) + 2 * j) =
+            u32x2{elem_pack<E>(x[j], x[j + 1]), elem_pack<E>(x[j + 2], x[j + 3])};
+    }
+  }
+  const int token = r / a.G;
+  if (half == 0 && r < R) {
+    if (part >= 0) {
+      a.stat[(at_part * kTile + local) * 2] = m;
+      a.stat[(at_part * kTile + local) * 2 + 1] = total;
     } else if (a.lse) {
+      const size_t at_row = static_cast<size_t>(row0 + token) * a.Hq + h * a.G + r % a.G;
       a.lse[at_row] = m == -INFINITY && total == 0.0f ? -INFINITY : (m - kLift + __builtin_amdgcn_logf(total)) * kLn2;
     }
+  }
+  if (part >= 0) return;
+  constexpr int kLanes = D / 8, kRows = 64 / kLanes;  // lanes of a row, rows of a store
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int i = 0; i < 32; i += kRows) {
+    const int row = i + lane / kLanes, its = tile * kTile + wave * 32 + row, its_token = __shfl(token, row);
+    const u32x4 x = *reinterpret_cast<const u32x4*>(stage + row * kStageRow<D> + lane % kLanes * 16);
+    const size_t at_row = static_cast<size_t>(row0 + its_token) * a.Hq + h * a.G + (its - its_token * a.G);
+    if (its < R) *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + at_row * D + lane % kLanes * 8) = x;
   }
 }
 
@@ -554,48 +579,20 @@ __device__ __forceinline__ void attend_piece(const ChunkArgs& a, int h, int at, 
   const int tile_least = limit_at(tile * kTile), tile_most = limit_at(last);
   const int wave_least = busy ? limit_at(wave_row) : 0, wave_most = busy ? limit_at(wave_last) : 0;
   const int limit = r < R ? limit_at(r) : 0;
-  f16x8 q[kSteps];
-  float cm;
+  // Ids of the next view pages, one a lane: now those of v_ids .., then the 64 after these.  (Loads through the scalar
+  // cache would wait for LDS reads and these for them.)
+  const auto ids_of = [&](int v) { return v0 < v1 ? table[view.page(v + lane < v1 ? v + lane : v1 - 1)] : 0; };
+  int v_ids = v0, ids = ids_of(v0), more_ids = ids_of(v0 + 64);
+  // The first ids, the queries and the first page's codes are on the way together: each latency in turn would cost a
+  // piece about as much as a page.
+  u32x4 q_words[kSteps];
   {
     const int token = r < R ? r / a.G : 0, hq = r < R ? h * a.G + r % a.G : 0;
     const uint16_t* src = a.q + static_cast<int64_t>(row0 + token) * a.row + hq * a.head + 8 * half;
-    u32x4 w[kSteps];
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) w[s] = r < R ? *reinterpret_cast<const u32x4*>(src + 16 * s) : u32x4{0u, 0u, 0u, 0u};
-    float factor = 1.0f;
-    if constexpr (std::is_same_v<E, BF16>) {
-      // To fp16's range by the power of two that brings the row's greatest value to 2^14 .. 2^15:
-      // values down to 2^-31 of it keep all their bits, the rest is off by 2^-39 of it at most.
-      float amax = 0.0f;
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float lo = fabsf(elem_lo<E>(w[s][j])), hi = fabsf(elem_hi<E>(w[s][j]));
-          amax = lo < INFINITY ? fmaxf(amax, lo) : amax;
-          amax = hi < INFINITY ? fmaxf(amax, hi) : amax;
-        }
-      amax = max_over_halves(amax);
-      int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-      ex = ex < -100 ? -100 : ex;
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[s][j] = elem_pack<F16>(ldexpf(elem_lo<E>(w[s][j]), 14 - ex), ldexpf(elem_hi<E>(w[s][j]), 14 - ex));
-      factor = ldexpf(1.0f, ex - 14);
-    }
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) q[s] = __builtin_bit_cast(f16x8, w[s]);
-    cm = fmaxf(a.scale * a.c.gk * kLog2e * factor, kMinNormal);
-    // The loop must not wait for these again, and with them for the next page.
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
+    for (int s = 0; s < kSteps; ++s) q_words[s] = r < R ? *reinterpret_cast<const u32x4*>(src + 16 * s) : u32x4{0u, 0u, 0u, 0u};
   }
-  float m = -INFINITY, l = 0.0f, l_over = 0.0f;  // l_over: what rounding put into l beyond the weights' sum
-  f32x16 o[DB];
-#pragma unroll
-  for (int d = 0; d < DB; ++d) o[d] = f32x16{};
-
+  __builtin_amdgcn_sched_barrier(0);
   // A page that the table does not name is read as the last one and seen by nobody.
   Raw<D> raws[kDeep];
   // The lane, found again for each page where the addresses made of it would take registers all the while.
@@ -605,10 +602,6 @@ __device__ __forceinline__ void attend_piece(const ChunkArgs& a, int h, int at, 
     return l;
   };
   const auto named = [&](int id) { return static_cast<unsigned>(id) < static_cast<unsigned>(a.c.pages); };
-  // Ids of the next view pages, one a lane: now those of v_ids .., then the 64 after these.  (Loads through the scalar
-  // cache would wait for LDS reads and these for them.)
-  const auto ids_of = [&](int v) { return v0 < v1 ? table[view.page(v + lane < v1 ? v + lane : v1 - 1)] : 0; };
-  int v_ids = v0, ids = ids_of(v0), more_ids = ids_of(v0 + 64);
   const auto page_id = [&](int v) { return __builtin_amdgcn_readlane(ids, v - v_ids); };
   const uint8_t* blocks = static_cast<const uint8_t*>(a.c.data) + static_cast<size_t>(h) * KvBlock<D>::kBytes;
   const uint32_t page_bytes = static_cast<uint32_t>(a.c.Hk) * KvBlock<D>::kBytes;
@@ -634,13 +627,58 @@ __device__ __forceinline__ void attend_piece(const ChunkArgs& a, int h, int at, 
   };
   int id[4] = {0, 0, 0, 0};  // of pages v .. v + 3
   if (v0 < v1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) id[i] = page_id(v0 + i);
+    load(raws[0], id[0], id[0]);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  f16x8 q[kSteps];
+  float cm;
+  {
+    float factor = 1.0f;
+    if constexpr (std::is_same_v<E, BF16>) {
+      // To fp16's range by the power of two that brings the row's greatest value to 2^14 .. 2^15:
+      // values down to 2^-31 of it keep all their bits, the rest is off by 2^-39 of it at most.
+      float amax = 0.0f;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float lo = fabsf(elem_lo<E>(q_words[s][j])), hi = fabsf(elem_hi<E>(q_words[s][j]));
+          amax = lo < INFINITY ? fmaxf(amax, lo) : amax;
+          amax = hi < INFINITY ? fmaxf(amax, hi) : amax;
+        }
+      amax = max_over_halves(amax);
+      int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+      ex = ex < -100 ? -100 : ex;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          q_words[s][j] = elem_pack<F16>(ldexpf(elem_lo<E>(q_words[s][j]), 14 - ex), ldexpf(elem_hi<E>(q_words[s][j]), 14 - ex));
+      factor = ldexpf(1.0f, ex - 14);
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      q[s] = __builtin_bit_cast(f16x8, q_words[s]);
+      // (Opaque: the loop, otherwise the same, gets other registers, and takes 2% less with bf16, 1% with the widest
+      // heads; with fp16 and D = 128 it takes 1.5% more.)
+      if constexpr (std::is_same_v<E, BF16> || D == 256) asm volatile("" : "+v"(q[s]));
+    }
+    cm = fmaxf(a.scale * a.c.gk * kLog2e * factor, kMinNormal);
+    // The loop must not wait for these again, and with them for the next page.
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
+  }
+  float m = -INFINITY, l = 0.0f, l_over = 0.0f;  // l_over: what rounding put into l beyond the weights' sum
+  f32x16 o[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d) o[d] = f32x16{};
+
+  if (v0 < v1) {
     // The first products are of no weights with the values of no page.
     uint32_t zero = 0u;
     asm volatile("" : "+v"(zero));
     for (int i = threadIdx.x; i < D * Tile<D>::kValueRow / 8; i += kThreads) *reinterpret_cast<u32x4*>(tiles[1].v + 8 * i) = u32x4{zero, zero, zero, zero};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) id[i] = page_id(v0 + i);
-    load(raws[0], id[0], id[0]);
     if constexpr (kWaits) {
       arrive();
       waiting.arrived(&raws[0], wave, here());
@@ -849,7 +887,11 @@ __device__ __forceinline__ void attend_piece(const ChunkArgs& a, int h, int at, 
   }
   if (flagged >= 0) add_bad(tiles[last_odd]);
   if (wave < kWaves / 2) lds_barrier();
-  store_rows<D, E>(arguments(), here(), wave, h, row0, R, tile, part, m, l, nan_groups[wave * 32 + (here() & 31)], o);
+  if (part < 0) lds_barrier();  // all have done with the tiles, where the rows wait to be stored
+  static_assert(kWaves * 32 * kStageRow<D> <= sizeof(shared.tiles));
+  if (busy)
+    store_rows<D, E>(arguments(), here(), wave, h, row0, R, tile, part, m, l, nan_groups[wave * 32 + (here() & 31)], o,
+                     reinterpret_cast<uint8_t*>(&tiles[0]) + wave * 32 * kStageRow<D>);
 }
 
 template <int D, class E>
@@ -864,26 +906,30 @@ __global__ __launch_bounds__(kThreads, 2) void chunk(const ChunkArgs a) {
   }
 }
 
-// Adds the pieces of cut tiles: D / 4 threads have a row, eight pieces' loads at a time.
+// Adds the pieces of cut tiles: a wavefront has a unit of them, kBatch pieces' loads at a time.
 template <int D, class E>
 __global__ __launch_bounds__(256) void chunk_join(const ChunkArgs a) {
-  constexpr int kPer = D / 4, kRows = 256 / kPer, kBatch = 8;
+  constexpr int kQuarters = D / 64, kBatch = D == 256 ? 4 : 8;
   const int at = static_cast<int>(blockIdx.x) / a.c.Hk, h = static_cast<int>(blockIdx.x) % a.c.Hk;
   if (at >= uniform_load(a.counts, 1)) return;
   const Cut sp = a.cut[at];
-  const int local = blockIdx.y * kRows + threadIdx.x / kPer, r = sp.tile * kTile + local, pos = threadIdx.x % kPer * 4;
+  const int lane = threadIdx.x & 63, unit = static_cast<int>(blockIdx.y) * 4 + static_cast<int>(threadIdx.x >> 6);
+  const int local = unit / 8 * 32 + (lane & 31), r = sp.tile * kTile + local, c = first_position(unit % 8, lane >> 5);
   if (r >= sp.T * a.G) return;
   float mm = -INFINITY, total = 0.0f;
-  f32x4 x{0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4 x[kQuarters];
+#pragma unroll
+  for (int q = 0; q < kQuarters; ++q) x[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   for (int s0 = 0; s0 < sp.pieces; s0 += kBatch) {
     float2 st[kBatch];
-    f32x4 v[kBatch];
+    f32x4 v[kBatch][kQuarters];
 #pragma unroll
     for (int s = 0; s < kBatch; ++s) {
       const int piece = s0 + s < sp.pieces ? s0 + s : s0;
-      const size_t p = (static_cast<size_t>(h) * a.parts + sp.part + piece) * kTile + local;
-      st[s] = *reinterpret_cast<const float2*>(a.stat + p * 2);
-      v[s] = *reinterpret_cast<const f32x4*>(a.part + p * D + pos);
+      const size_t p = static_cast<size_t>(h) * a.parts + sp.part + piece;
+      st[s] = *reinterpret_cast<const float2*>(a.stat + (p * kTile + local) * 2);
+#pragma unroll
+      for (int q = 0; q < kQuarters; ++q) v[s][q] = *reinterpret_cast<const f32x4*>(a.part + part_at<D>(p, unit, q, lane));
     }
 #pragma unroll
     for (int s = 0; s < kBatch; ++s)
@@ -894,13 +940,19 @@ __global__ __launch_bounds__(256) void chunk_join(const ChunkArgs a) {
         const float f0 = __builtin_amdgcn_exp2f(mm - about), f = __builtin_amdgcn_exp2f(st[s].x - about);
         mm = to;
         total = total * f0 + f * st[s].y;
-        x = x * f0 + f * v[s];
+#pragma unroll
+        for (int q = 0; q < kQuarters; ++q) x[q] = x[q] * f0 + f * v[s][q];
       }
   }
   const size_t at_row = static_cast<size_t>(sp.first + r / a.G) * a.Hq + h * a.G + r % a.G;
-  x *= mm == -INFINITY ? 0.0f : a.c.gv / total;
-  *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at_row * D + pos) = u32x2{elem_pack<E>(x[0], x[1]), elem_pack<E>(x[2], x[3])};
-  if (pos == 0 && a.lse) a.lse[at_row] = mm == -INFINITY && total == 0.0f ? -INFINITY : (mm - kLift + __builtin_amdgcn_logf(total)) * kLn2;
+  const float inv = mm == -INFINITY ? 0.0f : a.c.gv / total;
+#pragma unroll
+  for (int q = 0; q < kQuarters; ++q) {
+    x[q] *= inv;
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at_row * D + c * (D / 16) + 4 * q) =
+        u32x2{elem_pack<E>(x[q][0], x[q][1]), elem_pack<E>(x[q][2], x[q][3])};
+  }
+  if (c == 0 && a.lse) a.lse[at_row] = mm == -INFINITY && total == 0.0f ? -INFINITY : (mm - kLift + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
@@ -925,7 +977,7 @@ ChunkPlan kv4_chunk_plan(int N, int B, int Hq, int Hk, int D, int width, int win
     return p;
   }
   // Of g workgroups in a row at most g - 1 begin inside a tile, and each of these cuts makes one piece more.
-  const int64_t slots = slots_per_head(Hk), even = (p.tiles * pages + kLeast - 1) / kLeast;
+  const int64_t slots = slots_per_head(Hk), even = (p.tiles * (pages + kBegin) + kLeast - 1) / kLeast;
   const int64_t inside = slots < 4 ? 0 : (slots < even ? slots : even) - 1;
   p.cuts = p.tiles < inside ? p.tiles : inside;
   p.parts = p.cuts + inside;
@@ -957,7 +1009,7 @@ hipError_t launch_kv4_chunk(const kv4_cache& c, const void* q, int64_t row, int6
   const auto run = [&](auto d, auto e) {
     chunk<d(), decltype(e)><<<dim3(static_cast<unsigned>(p.groups * c.Hk)), kThreads, 0, stream>>>(a);
     if (p.cuts)
-      chunk_join<d(), decltype(e)><<<dim3(static_cast<unsigned>(p.cuts * c.Hk), kTile * d() / 1024), 256, 0, stream>>>(a);
+      chunk_join<d(), decltype(e)><<<dim3(static_cast<unsigned>(p.cuts * c.Hk), kTile / 16), 256, 0, stream>>>(a);
   };
   const auto by_type = [&](auto d) {
     if (type == SKINNY_F16) run(d, F16());
