@@ -31,7 +31,7 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kTile = 32 * kWaves;
 constexpr int kSlots = 256;  // workgroups that the CUs hold at once
 constexpr int kLeast = 16;   // fewest pages of a workgroup where tiles are cut
-constexpr int kCutPages = 24;  // what the cut tiles' parts cost a workgroup, in pages: stored by it, and read by the join
+constexpr int kCutPages = 6;  // what the cut tiles' parts cost a workgroup, in pages: stored by it, and read by the join
 constexpr int kBegin = 10;     // what a tile's beginning and end cost, in pages (less than kLeast; see the plan)
 constexpr int kPlanThreads = 256;
 constexpr int kPlanHeld = 1024;  // sequences whose rows and tiles the plan keeps in LDS
@@ -131,7 +131,10 @@ struct Sight {
 // pages more than it has, or the workgroup with the shortest tiles, up to eleven of
 // them, ends last: 16 chunks of 1 .. 640 tokens over up to 9000, five draws, took
 // 514, 369, 424, 419 and 344 us with 0, 476, 343, 362, 362 and 283 with 5, 468, 338,
-// 359, 336 and 260 with 10, and 470, 341, 355, 334 and 262 with 14.
+// 359, 336 and 260 with 10, and 470, 341, 355, 334 and 262 with 14.  Whole tiles are
+// taken where they end kCutPages or less after the even shares: three chunks of 1500
+// .. 4100 tokens within 1024 (D = 256), 382, 360, 340 and 356 us as whole tiles (24
+// or 12 pages), 373, 331, 323 and 327 cut; 14 chunks of 1286 the same either way.
 //
 // The rows of a sequence go from its start to the next one's; a start that is not
 // in 0 .. N counts as the nearer of these, and one below an earlier start as that:
