@@ -15,6 +15,22 @@
 // hold its column.  The first product takes the tokens of a tile of 32 in the
 // order that leaves lane 32 h + c with row c's tokens 8 h .. 8 h + 7 of every 16,
 // which is the second one's right operand.
+//
+// Two wavefronts share a SIMD, and those of one half of the workgroup run a barrier
+// behind the other's: one has the matrix unit for its products, between which it
+// widens its part of the next page, while the other has the VALU for its softmax.
+// Operands come from LDS, six products ahead of their use.  256 rows are what one
+// workgroup a CU holds in registers (D = 128: 64 of sums, 32 of queries, 32 of
+// scores a lane), and each row more shares the widening of a page, 42 to 64 VALU
+// operations a lane and 36 KB of LDS writes.
+//
+// Bound by the matrix unit, the VALU and the power that both may draw: 8192 tokens,
+// 48 + 4 heads of 128, 810 .. 855 us, 0.98 .. 1.02 PFLOP/s of seen products at
+// about 1.8 GHz, where a large fp16 product reaches 1.0 PFLOP/s at first and 1.36
+// when nothing else runs for long.  The matrix unit is busy for 53% of the cycles,
+// the VALU for 58%, LDS for 37%.  Parts left out of the kernel of 852 us (for
+// timing only): softmax 127 us, of which the exponentials 89; widening 92; operand
+// reads 58; all but products and widening, 658 us are left.
 #include <hip/hip_runtime.h>
 
 #include "kv4.cuh"
@@ -489,7 +505,7 @@ template <int D>
 constexpr int kStageRow = 2 * D + 16;  // bytes: rows are 16 off the banks' period
 
 // A wavefront's rows, or its part of them where the tile is split.  Whole rows go through LDS to be stored 1024 bytes at
-// a time; from the lanes' own positions every store meets 32 rows, and a tile's took as long as four of its pages.
+// a time; from the lanes' own positions every store meets 32 rows (D = 256, 202 tiles a head: 372 against 368 us).
 template <int D, class E>
 __device__ __forceinline__ void store_rows(const ChunkArgs& a, int lane, int wave, int h, int row0, int R, int tile, int part, float m, float l,
                                            uint32_t nan_groups, f32x16 (&o)[D / 32], uint8_t* stage) {
@@ -586,8 +602,8 @@ __device__ __forceinline__ void attend_piece(const ChunkArgs& a, int h, int at, 
   // cache would wait for LDS reads and these for them.)
   const auto ids_of = [&](int v) { return v0 < v1 ? table[view.page(v + lane < v1 ? v + lane : v1 - 1)] : 0; };
   int v_ids = v0, ids = ids_of(v0), more_ids = ids_of(v0 + 64);
-  // The first ids, the queries and the first page's codes are on the way together: each latency in turn would cost a
-  // piece about as much as a page.
+  // The first ids, the queries and the first page's codes are on the way together (six tiles a workgroup's place one
+  // after another: 829 us, and 815 so).
   u32x4 q_words[kSteps];
   {
     const int token = r < R ? r / a.G : 0, hq = r < R ? h * a.G + r % a.G : 0;
@@ -909,7 +925,8 @@ __global__ __launch_bounds__(kThreads, 2) void chunk(const ChunkArgs a) {
   }
 }
 
-// Adds the pieces of cut tiles: a wavefront has a unit of them, kBatch pieces' loads at a time.
+// Adds the pieces of cut tiles: a wavefront has a unit of them, kBatch pieces' loads at a time.  Bound by memory: 31 cut
+// tiles of 8 heads, 65 MB of parts in 16 us (of rows that lie together, 18).
 template <int D, class E>
 __global__ __launch_bounds__(256) void chunk_join(const ChunkArgs a) {
   constexpr int kQuarters = D / 64, kBatch = D == 256 ? 4 : 8;
