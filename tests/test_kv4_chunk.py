@@ -7,7 +7,7 @@ import torch
 import fp8_quantized_skinny_amd as sk
 from fp8_quantized_skinny_amd._lib import lib
 from oracle import kv4 as oracle
-from test_kv4 import A, BAD_CACHES, HALF_STEP, MIS, TYPES, _attend_inputs, _cache, _cuda
+from test_kv4 import A, BAD_CACHES, HALF_STEP, MIS, TYPES, _attend_inputs, _cache, _cuda, _random_cache
 
 gpu = pytest.mark.gpu
 
@@ -427,3 +427,30 @@ def test_many_slots_of_little_weight_count(D, call):
     # a score's fp32 roundings, the exponential's of numbers up to 64, and the log-sum's own: 2^-24 of 64 each, sixteen of them
     assert (np.abs(lse.double().cpu().numpy().reshape(len(limits), Hq) - want[:, None]) <= 16 * 64 * 2.0 ** -24).all()
     assert (out.double() - 1.0).abs().max().item() <= 2.0 ** -8
+
+
+@gpu
+@pytest.mark.parametrize("B, longest", [(300, 190000), (1100, 500), (1500, 100000)])
+def test_many_sequences(B, longest):
+    """More tiles than the plan has threads, more sequences than it holds at once, and one that is much longer than all
+    others, or not; some have no new token, and pages are shared."""
+    rng = np.random.default_rng(B)
+    D, Hq, Hk = 64, 8, 8
+    chunks = rng.integers(0, 4, B)
+    lens = np.maximum(chunks, rng.integers(0, 130, B))
+    at = B // 2
+    chunks[at], lens[at] = 3, longest
+    width = max(100, -(-longest // 64))
+    cache = _random_cache(rng, 40, Hk, D)
+    table = rng.integers(-1, len(cache), (B, width)).astype(np.int32)
+    starts = np.concatenate([[2], 2 + np.cumsum(chunks)]).astype(np.int32)
+    N = int(starts[-1]) + 3
+    q = torch.from_numpy(rng.standard_normal((N, Hq, D)) * 2.0).half()
+    out, lse = torch.full((N, Hq, D), 3.0, dtype=torch.float16, device="cuda"), torch.full((N, Hq), 3.0, device="cuda")
+    ws = sk.new_workspace(sk.kv4_attention_chunk_workspace_bytes(N, B, Hq, Hk, D, width))
+    sk.kv4_attention_chunk(q.cuda(), _cuda(starts), _cuda(cache), _cuda(table), _cuda(lens.astype(np.int32)), out, lse=lse, scale=0.125, workspace=ws)
+    for t in (out, lse):
+        assert (t[:2] == 3).all() and (t[N - 3:] == 3).all()
+    some = [(b, i, rng.integers(Hq)) for b in [at, *rng.permutation(B)[:150], 0, B - 1] for i in range(chunks[b])]
+    _check("f16", out, lse, _refs(some, cache, table, lens, starts, q.double().numpy(), Hq, Hk, D, 0.125, 1.0, 1.0, 0, 0))
+    assert not (out[2:N - 3] == 3).all(-1).any()
