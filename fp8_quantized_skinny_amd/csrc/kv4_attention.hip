@@ -36,6 +36,12 @@ constexpr float kMinNormal = 0x1p-126f;
 // down to 2^-20 of the greatest, and a row's sums are rescaled rarely.
 constexpr float kLift = 6.0f, kSlack = 8.0f;
 
+struct ChunkSegment {  // a group of rows of a sequence, for the join of its shares
+  int first, splits;   // its first share and their number; the next is Hk further
+  int row0, r0, R;     // the sequence's first token among all, the group's first row in it, and the sequence's rows
+  int pad[3];
+};
+
 struct AttendArgs {
   kv4_cache c;
   kv4_rows q;
@@ -50,6 +56,8 @@ struct AttendArgs {
   int window, sinks;  // windowed calls: a row with limit L sees the slots from L - window on, and those below sinks
   const int32_t* starts;  // chunks of another length for each sequence: their rows (see kv4_attention_chunk), of N
   int N;
+  ChunkSegment* segments;  // [group][Hk] where chunks are split, and the number of groups; otherwise null
+  int* count;
 };
 
 // The pages that rows with limits from `least` to `most` see: all up to the
@@ -361,45 +369,93 @@ __device__ __forceinline__ Share plan_share(const AttendArgs& a, int lane) {
   return s;
 }
 
-// Chunks: a workgroup has a group of `rows` rows of a head and all pages that they
-// see.  The rows of a sequence go from its start to the next one's, as in
-// kv4_chunk.hip: starts are held to 0 .. N and to what came before them.
+// Chunks: a workgroup has a group of `rows` rows of a head and the pages that they
+// see, or a share of these.  The rows of a sequence go from its start to the next
+// one's, as in kv4_chunk.hip: starts are held to 0 .. N and to what came before
+// them.  Shares are found as above, but for a sequence's groups alike: as many as
+// the pages of its last group want, of which no other has more.  Of a group of rows
+// that see fewer the last shares may be left without a page, and add nothing.
 struct ChunkRows {
-  int T, row0;  // the sequence's tokens, and its first row
+  int T, row0;      // the sequence's tokens, and its first row
+  int end, group;   // where the share's pages end, and the group among all sequences'
 };
 __device__ __forceinline__ Share chunk_share(const AttendArgs& a, int rows, int lane, ChunkRows* of) {
-  const int at = static_cast<int>(blockIdx.x) / a.c.Hk;
+  const int at = static_cast<int>(blockIdx.x) / a.c.Hk, B = a.c.B;
   const auto held = [&](int s, int least) { return s < least ? least : (s > a.N ? a.N : s); };
+  struct Sequence {
+    int begin, end, n, pages, len;  // its rows, groups of these, and the pages that they see
+  };
+  // Of sequence b0 + lane; `start` goes from the first one's to the next ones'.
+  const auto sequence = [&](int b0, int& start) {
+    const int b = b0 + lane;
+    Sequence s{0, 0, 0, 0, 0};
+    s.end = held(b < B ? a.starts[b + 1] : 0, start);
+    for (int o = 1; o < 64; o <<= 1) {
+      const int x = __shfl_up(s.end, o);
+      if (lane >= o && x > s.end) s.end = x;
+    }
+    const int up = __shfl_up(s.end, 1);
+    s.begin = lane ? up : start;
+    if (b < B) {
+      s.n = static_cast<int>((static_cast<int64_t>(s.end - s.begin) * a.G + rows - 1) / rows);
+      s.len = kv_len(a.c, b);
+      const int tokens = s.end - s.begin < rows ? s.end - s.begin : rows, least = s.len - (tokens - 1);
+      const View<true> view(a, least < 0 ? 0 : least, s.len);
+      s.pages = view.pages() + (view.from > 0);  // another group's window may lie across one page more
+    }
+    start = __builtin_amdgcn_readlane(s.end, 63);
+    return s;
+  };
+  const int start0 = held(uniform_load(a.starts, 0), 0);
+  int after0 = start0;
+  const Sequence first = sequence(0, after0);
+  int chunk = 0;
+  const auto shares = [&](const Sequence& s) { return chunk && s.pages > chunk ? s.n * ((s.pages + chunk - 1) / chunk) : s.n; };
+  const auto sum = [&](auto of_sequence) {
+    int start = after0, all = 0;
+    for (int b0 = 0; b0 < B; b0 += 64) all += __builtin_amdgcn_readlane(wave_scan(of_sequence(b0 ? sequence(b0, start) : first)), 63);
+    return all;
+  };
+  if (a.segments) {
+    const int room = static_cast<int>(gridDim.x) / a.c.Hk, groups = sum([](const Sequence& s) { return s.n; });
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.count = groups;
+    chunk = sum([](const Sequence& s) { return s.n * s.pages; }) / (room - (groups >> 1)) + 1;
+    chunk = chunk < a.least ? a.least : chunk;
+    while (sum(shares) > room) chunk += (chunk >> 4) + 1;
+  }
   Share s;
   s.any = false;
   s.h = static_cast<int>(blockIdx.x) % a.c.Hk;
   s.b = s.qg = s.len = s.p0 = s.p1 = s.first = 0;
   s.splits = 1;
-  int start = held(uniform_load(a.starts, 0), 0), before = 0;
-  for (int b0 = 0; b0 < a.c.B; b0 += 64) {
-    const int b = b0 + lane;
-    int end = held(b < a.c.B ? a.starts[b + 1] : 0, start);
-    for (int o = 1; o < 64; o <<= 1) {
-      const int x = __shfl_up(end, o);
-      if (lane >= o && x > end) end = x;
-    }
-    const int up = __shfl_up(end, 1), begin = lane ? up : start;
-    const int n = b < a.c.B ? static_cast<int>((static_cast<int64_t>(end - begin) * a.G + rows - 1) / rows) : 0;
-    const int upto = before + wave_scan(n), last = __builtin_amdgcn_readlane(upto, 63);
+  of->end = of->group = 0;
+  int before = 0, groups = 0;
+  for (int b0 = 0, start = after0; b0 < B; b0 += 64) {
+    const Sequence q = b0 ? sequence(b0, start) : first;
+    const int all = shares(q), upto = before + wave_scan(all), group = groups + wave_scan(q.n), last = __builtin_amdgcn_readlane(upto, 63);
     if (at < last) {
       const int l = __popcll(__ballot(upto <= at));  // the lane of the sequence
+      const auto its = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
       s.any = true;
       s.b = b0 + l;
-      s.qg = at - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(n, l));
-      of->row0 = __builtin_amdgcn_readlane(begin, l);
-      of->T = __builtin_amdgcn_readlane(end, l) - of->row0;
-      s.len = kv_len_uniform(a.c, __builtin_amdgcn_readfirstlane(s.b));
+      s.splits = its(all) / its(q.n);
+      const int in = at - (its(upto) - its(all));  // among the sequence's shares
+      s.qg = in / s.splits;
+      const int each = (its(q.pages) + s.splits - 1) / s.splits, share = in % s.splits;
+      of->group = its(group) - its(q.n) + s.qg;
+      s.p0 = share * each;
+      of->end = share == s.splits - 1 ? 0x7FFFFFFF : s.p0 + each;  // the last one's: what there is
+      s.first = (at - share) * a.c.Hk + s.h;
+      of->row0 = its(q.begin);
+      of->T = its(q.end) - of->row0;
+      s.len = its(q.len);
       break;
     }
     before = last;
-    start = __builtin_amdgcn_readlane(end, 63);
+    groups = __builtin_amdgcn_readlane(group, 63);
   }
-  for (int* f : {&s.b, &s.h, &s.qg, &s.len}) *f = __builtin_amdgcn_readfirstlane(*f);
+  for (int* f : {&s.b, &s.h, &s.qg, &s.len, &s.p0, &s.splits, &s.first, &of->end, &of->group, &of->row0, &of->T})
+    *f = __builtin_amdgcn_readfirstlane(*f);
   return s;
 }
 
@@ -443,7 +499,7 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
   __shared__ float stat[kWaves][MT * 16][2];
   __shared__ __align__(16) float sums[kWaves][D * 16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, c = lane & 15;
-  ChunkRows of{a.T, 0};
+  ChunkRows of{a.T, 0, 0, 0};
   Share sh = CHUNK ? chunk_share(a, MT * 16, lane, &of) : plan_share<WINDOW>(a, lane);
   if (!sh.any) return;
   const int b = sh.b, h = sh.h, qg = sh.qg, len = sh.len;
@@ -462,11 +518,13 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
     rows.data = static_cast<const uint16_t*>(rows.data) + of.row0 * rows.row;
     rows.sequence = 0;
   }
+  if (CHUNK && a.segments && sh.first == static_cast<int>(blockIdx.x) && threadIdx.x == 0)
+    a.segments[of.group * a.c.Hk + h] = ChunkSegment{sh.first, sh.splits, of.row0, qg * MT * 16, R, {}};
   if (!CHUNK && a.split && sh.first == static_cast<int>(blockIdx.x) && threadIdx.x == 0)
     a.split[(b * a.c.Hk + h) * a.QG + qg] = int2{sh.first, sh.splits};
   const int32_t* table = a.c.table + static_cast<size_t>(b) * a.c.width;
   const View<WINDOW> view(a, least, most);
-  if constexpr (CHUNK) sh.p1 = view.pages();
+  if constexpr (CHUNK) sh.p1 = of.end < view.pages() ? of.end : view.pages();
   int page = sh.p0 + wave;  // of those that the sequence's rows see
   Queries<D, MT> q;
   q.load(rows, b, h, qg, a.G, R);
@@ -690,16 +748,33 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
 // loads at a time, and the sets meet in LDS.  33 shares of 384 rows (one
 // sequence of 8197 tokens, eight rows of 48 heads): 9.7 us with one set, 5.2
 // with eight.
-template <int D, int MT, class E>
+template <int D, int MT, class E, bool CHUNK>
 __global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a) {
   constexpr int kPer = D / 4, kSets = kThreads / kPer, kBatch = 8;
   __shared__ f32x4 sums[kSets][kPer];
   __shared__ float2 stats[kSets];
   const int segment = blockIdx.x, local = blockIdx.y;
-  const int qg = segment % a.QG, h = segment / a.QG % a.c.Hk, b = segment / a.QG / a.c.Hk, stride = a.c.Hk * a.QG;
-  const int r = qg * MT * 16 + local;
-  if (r >= a.T * a.G) return;
-  const int2 split = a.split[segment];
+  int h, r, stride;
+  size_t token0;  // the first of the segment's sequence, among all rows
+  int2 split;
+  if constexpr (CHUNK) {
+    if (segment / a.c.Hk >= *a.count) return;
+    const ChunkSegment s = a.segments[segment];
+    h = segment % a.c.Hk;
+    r = s.r0 + local;
+    stride = a.c.Hk;
+    token0 = s.row0;
+    split = int2{s.first, s.splits};
+    if (r >= s.R) return;
+  } else {
+    const int qg = segment % a.QG, b = segment / a.QG / a.c.Hk;
+    h = segment / a.QG % a.c.Hk;
+    r = qg * MT * 16 + local;
+    stride = a.c.Hk * a.QG;
+    token0 = static_cast<size_t>(b) * a.T;
+    if (r >= a.T * a.G) return;
+    split = a.split[segment];
+  }
   if (split.y <= 1) return;
   const int set = threadIdx.x / kPer, at = threadIdx.x % kPer;
   const auto row = [&](int s) { return (static_cast<size_t>(split.x) + static_cast<size_t>(s) * stride) * (MT * 16) + local; };
@@ -734,7 +809,7 @@ __global__ __launch_bounds__(kThreads) void attend_join(const AttendArgs a) {
   if (set != 0) return;
 #pragma unroll
   for (int s = 1; s < kSets; ++s) add(stats[s].x, stats[s].y, sums[s][at]);
-  const size_t at_row = (static_cast<size_t>(b) * a.T + r / a.G) * a.Hq + h * a.G + r % a.G;
+  const size_t at_row = (token0 + r / a.G) * a.Hq + h * a.G + r % a.G;
   x *= mm == -INFINITY ? 0.0f : a.c.gv / total;
   *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at_row * D + at * 4) =
       u32x2{elem_pack<E>(x[0], x[1]), elem_pack<E>(x[2], x[3])};
@@ -939,7 +1014,7 @@ hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type,
                                 int sinks, void* out, float* lse, void* workspace, hipStream_t stream) {
   const AttendPlan p = kv4_attend_plan(c.B, T, Hq, c.Hk, c.D, c.width, window, sinks);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  AttendArgs a{c, q, out, lse, nullptr, nullptr, nullptr, T, Hq, Hq / c.Hk, p.QG, p.least, scale, window, sinks, nullptr, 0};
+  AttendArgs a{c, q, out, lse, nullptr, nullptr, nullptr, T, Hq, Hq / c.Hk, p.QG, p.least, scale, window, sinks, nullptr, 0, nullptr, nullptr};
   if (p.split) {
     a.part = reinterpret_cast<float*>(ws + p.part_off);
     a.stat = reinterpret_cast<float*>(ws + p.stat_off);
@@ -951,40 +1026,85 @@ hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type,
     if (window) attend<d(), mt(), decltype(e), true, false><<<grid, kThreads, 0, stream>>>(a);
     else attend<d(), mt(), decltype(e), false, false><<<grid, kThreads, 0, stream>>>(a);
     if (p.split)
-      attend_join<d(), mt(), decltype(e)><<<dim3(segments, mt() * 16), kThreads, 0, stream>>>(a);
+      attend_join<d(), mt(), decltype(e), false><<<dim3(segments, mt() * 16), kThreads, 0, stream>>>(a);
   });
 }
 
-// Chunks of few rows over few pages: as kv4_attention, but every workgroup has all
-// the pages of its rows, so that one launch does.  The fewest tiles of rows per
-// workgroup that leave no more workgroups than the CUs hold at once: a page takes
-// a wavefront the less.  One launch against the tiles of 256 rows of kv4_chunk.hip
-// with their plan and join (D = 128, 8 heads of 4 query heads, 9 rows; us):
+// Chunks of few rows: as kv4_attention.  Over few pages every workgroup has all the
+// pages of its rows, so that one launch does: the fewest tiles of rows per
+// workgroup that leave no more workgroups than the CUs hold at once, as a page takes
+// a wavefront the less.  Against the tiles of 256 rows of kv4_chunk.hip with their
+// plan and join (D = 128, 8 heads of 4 query heads, 9 rows; us):
 //   pages        4    16    32    64   128   256
 //   this       7.0  11.1  16.7  27.0  47.3  87.3
 //   the other 17.0  32.8  55.5  36.5  37.2  39.6
 // and 16.1, 24.5, 40.3, 72.5 against 40.7, 64.7, 65.0, 74.9 with 256 rows and 16
 // to 128 pages.  The two meet near 96 pages there and for D = 64 (29 us), and
 // between 96 and 128 for D = 256.
+//
+// Over more pages these are split into shares.  Of many pages a group of 48 rows
+// (32 at D = 256) takes kGroup[D] ns a page and head of the whole card's time, a tile
+// of 256 rows with few of them in use kTileOf[D], which has a plan and other
+// beginnings to make up for, kFixed ns; shares are coarse where there are many groups.
+// Split against tiles of 256 rows, four heads of 12 (128) or 6 (256), us:
+//   sequences x rows, pages   D = 128: 128          512          2048    D = 256: 512
+//   1 x 48                    17.9  39.0   24.5  46.7   38.5  82.0    33.4  78.0
+//   1 x 252                   26.8  44.3   46.6  55.6    119  99.1    72.7  97.1
+//   1 x 960                   42.9  49.4    104  85.7    332   252     226   167
+//   16 x 48                   39.3  68.0   87.6   194    296   691     246   402
+//   16 x 120 or 126           89.0  74.4    260   209    919   718     461   438
+//   16 x 252                   126  91.4    391   254   1486   964     886   545
 SmallChunk kv4_small_chunk(int N, int B, int G, int Hk, int D, int64_t pages) {
   constexpr int kCUs = 256, kMostPages = 96;
-  SmallChunk s{0, 0};
-  if (pages > kMostPages) return s;
-  const int64_t busy = N < B ? N : B;  // sequences with rows
-  for (int mt = 1; mt <= max_tiles(D); ++mt) {
-    const int64_t groups = (static_cast<int64_t>(N) * G + busy * (mt * 16 - 1)) / (mt * 16);
-    if (groups * Hk <= kCUs * attend_per_cu(D, mt)) return SmallChunk{mt, groups};
-  }
+  SmallChunk s{};
+  const int64_t busy = N < B ? N : B, rows = static_cast<int64_t>(N) * G;  // sequences with rows
+  const auto groups = [&](int height) { return (rows + busy * (height - 1)) / height; };
+  if (pages <= kMostPages)
+    for (int mt = 1; mt <= max_tiles(D); ++mt)
+      if (groups(mt * 16) * Hk <= kCUs * attend_per_cu(D, mt)) {
+        s.tiles = mt;
+        s.groups = s.shares = groups(mt * 16);
+        return s;
+      }
+  const int64_t mean = (rows + busy - 1) / busy;  // rows of a sequence
+  const int mt = mean < max_tiles(D) * 16 ? static_cast<int>((mean + 15) / 16) : max_tiles(D);
+  const int64_t tall = groups(mt * 16);
+  if (pages <= kMostPages || tall * (pages + 1) > INT32_MAX) return s;
+  constexpr double kGroup[] = {1.6, 2.25, 3.2}, kTileOf[] = {3.9, 5.5, 11.3}, kFixed[] = {16000.0, 16000.0, 35000.0};
+  const int size = D / 128;  // 0, 1, 2
+  const int64_t whole = busy * ((mean + mt * 16 - 1) / (mt * 16));
+  const double split = kGroup[size] * whole, tiled = kTileOf[size] * (busy * ((mean + 255) / 256));
+  if (split * 1.15 > tiled && (whole * Hk > 128 || (split - tiled) * Hk * pages > kFixed[size])) return s;
+  s.tiles = mt;
+  s.groups = tall;
+  const int64_t room = kCUs * attend_per_cu(D, mt) / Hk, most = tall * ((pages + kWaves - 1) / kWaves);
+  s.shares = room < 2 * tall ? 2 * tall : room;
+  s.shares = s.shares < most ? s.shares : most;
+  const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  s.count_off = kSyncBytes;
+  s.segment_off = s.count_off + 256;
+  s.stat_off = s.segment_off + up(static_cast<size_t>(tall) * Hk * sizeof(ChunkSegment));
+  s.part_off = s.stat_off + static_cast<size_t>(s.shares) * Hk * mt * 16 * 8;
+  s.total = s.part_off + static_cast<size_t>(s.shares) * Hk * mt * 16 * D * 4;
   return s;
 }
 
 hipError_t launch_kv4_small_chunk(const kv4_cache& c, const void* q, int64_t row, int64_t head, const int32_t* starts, int N,
-                                  int type, int Hq, float scale, int window, int sinks, void* out, float* lse,
+                                  int type, int Hq, float scale, int window, int sinks, void* out, float* lse, void* workspace,
                                   const SmallChunk& s, hipStream_t stream) {
   const int wide = window ? window : c.width * kPage;  // a window that leaves nothing out
-  const AttendArgs a{c, {q, 0, row, head}, out, lse, nullptr, nullptr, nullptr, 0, Hq, Hq / c.Hk, 1, 0, scale, wide, sinks, starts, N};
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  AttendArgs a{c, {q, 0, row, head}, out, lse, nullptr, nullptr, nullptr, 0, Hq, Hq / c.Hk, 1, kWaves, scale, wide, sinks, starts, N, nullptr, nullptr};
+  if (s.total) {
+    a.part = reinterpret_cast<float*>(ws + s.part_off);
+    a.stat = reinterpret_cast<float*>(ws + s.stat_off);
+    a.segments = reinterpret_cast<ChunkSegment*>(ws + s.segment_off);
+    a.count = reinterpret_cast<int*>(ws + s.count_off);
+  }
   return by_shape(c.D, type, s.tiles, [](int D) constexpr { return max_tiles(D); }, [&](auto d, auto mt, auto e) {
-    attend<d(), mt(), decltype(e), true, true><<<dim3(static_cast<unsigned>(s.groups * c.Hk)), kThreads, 0, stream>>>(a);
+    attend<d(), mt(), decltype(e), true, true><<<dim3(static_cast<unsigned>(s.shares * c.Hk)), kThreads, 0, stream>>>(a);
+    if (s.total)
+      attend_join<d(), mt(), decltype(e), true><<<dim3(static_cast<unsigned>(s.groups * c.Hk), mt() * 16), kThreads, 0, stream>>>(a);
   });
 }
 

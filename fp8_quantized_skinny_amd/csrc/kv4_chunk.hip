@@ -992,8 +992,8 @@ ChunkPlan kv4_chunk_plan(int N, int B, int Hq, int Hk, int D, int width, int win
   }
   p.small = kv4_small_chunk(N, B, static_cast<int>(G), Hk, D, pages);
   if (p.small.tiles) {
-    p.groups = p.small.groups;
-    p.total = 0;
+    p.groups = p.small.shares;
+    p.total = p.small.total;
     return p;
   }
   // Of g workgroups in a row at most g - 1 begin inside a tile, and each of these cuts makes one piece more.
@@ -1018,7 +1018,7 @@ hipError_t launch_kv4_chunk(const kv4_cache& c, const void* q, int64_t row, int6
                             int Hq, float scale, int window, int sinks, void* out, float* lse, void* workspace, hipStream_t stream) {
   const ChunkPlan p = kv4_chunk_plan(N, c.B, Hq, c.Hk, c.D, c.width, window, sinks);
   if (p.small.tiles)
-    return launch_kv4_small_chunk(c, q, row, head, starts, N, type, Hq, scale, window, sinks, out, lse, p.small, stream);
+    return launch_kv4_small_chunk(c, q, row, head, starts, N, type, Hq, scale, window, sinks, out, lse, workspace, p.small, stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const ChunkArgs a{c, static_cast<const uint16_t*>(q), row, head, starts, out, lse, reinterpret_cast<int*>(ws + p.counts_off),
                     reinterpret_cast<int*>(ws + p.begin_off), reinterpret_cast<int*>(ws + p.offset_off), reinterpret_cast<int*>(ws + p.first_off),

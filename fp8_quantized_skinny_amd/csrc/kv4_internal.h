@@ -33,15 +33,17 @@ hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type,
                                 int sinks, void* out, float* lse, void* workspace, hipStream_t stream);
 hipError_t launch_kv4_weights(const kv4_cache& c, const kv4_rows& q, int type, int T, int Hq, float scale,
                               const float* lse, const float* acc, float* acc_out, hipStream_t stream);
-// A chunk call of few rows and pages: tiles of 16 rows per workgroup, 0 where it is
-// not one, and the most groups of these that there are.
+// A chunk call of few rows a sequence: tiles of 16 rows per workgroup, 0 where it is
+// not one, the most groups of these that there are, and shares of their pages, per
+// key/value head each; a workspace where groups are split.
 struct SmallChunk {
   int tiles;
-  int64_t groups;
+  int64_t groups, shares;
+  size_t count_off, segment_off, stat_off, part_off, total;
 };
 SmallChunk kv4_small_chunk(int N, int B, int G, int Hk, int D, int64_t pages);
 hipError_t launch_kv4_small_chunk(const kv4_cache& c, const void* q, int64_t row, int64_t head, const int32_t* starts, int N,
-                                  int type, int Hq, float scale, int window, int sinks, void* out, float* lse,
+                                  int type, int Hq, float scale, int window, int sinks, void* out, float* lse, void* workspace,
                                   const SmallChunk& s, hipStream_t stream);
 // How other chunk calls are laid out: the most tiles of rows, workgroups, tiles that are
 // cut and parts of them, each per key/value head, and the workspace.

@@ -76,16 +76,17 @@ CHUNKS = [  # type, D, Hq, Hk, chunks, lens, window, sinks
 ]
 
 
-WIDE = pytest.mark.parametrize("wide", [False, True])  # few rows over few pages, and any over a table of more than 96, go different ways
+# Three ways: few rows over few pages, few rows over a table of more than 96 pages, and many rows (most of them no sequence's).
+WIDE = pytest.mark.parametrize("wide", [False, True, "tall"])
 
 
 def _inputs(rng, kind, D, Hq, Hk, chunks, lens, wide, pad=3, q_size=2.0):
     """Pages as for the steps of a few rows, a wide table with 100 columns more that name none; packed queries in a qkv
-    GEMM's output, `pad` rows before the first and behind the last."""
+    GEMM's output, `pad` rows before the first and behind the last, and more of these where it is tall."""
     table, cache, _ = _attend_inputs(rng, kind, D, Hq, Hk, 1, lens)
     if wide:
         table = np.concatenate([table, np.full((len(lens), 100), -1, np.int32)], 1)
-    N = sum(chunks) + 2 * pad
+    N = sum(chunks) + 2 * pad + (500 * len(chunks) * Hk // Hq + 1 if wide == "tall" else 0)
     qkv = torch.from_numpy(rng.standard_normal((N, (Hq + 2 * Hk) * D)) * q_size).to(TYPES[kind])
     starts = pad + np.concatenate([[0], np.cumsum(chunks)]).astype(np.int32)
     return table, cache, qkv, starts
@@ -164,7 +165,7 @@ def test_a_prompt_agrees_with_its_last_rows_one_by_one(wide):
     rng = np.random.default_rng(2)
     D, Hq, Hk, n = 128, 16, 2, 1500
     table, cache, qkv, starts = _inputs(rng, "bf16", D, Hq, Hk, [n], [n], wide, pad=0)
-    q = qkv.cuda()[:, :Hq * D].unflatten(-1, (Hq, D))
+    q = qkv.cuda()[:n, :Hq * D].unflatten(-1, (Hq, D))
     c, t = _cuda(cache), _cuda(table)
     out, lse = torch.empty((n, Hq, D), dtype=torch.bfloat16, device="cuda"), torch.empty((n, Hq), device="cuda")
     ws = sk.new_workspace(sk.kv4_attention_chunk_workspace_bytes(n, 1, Hq, Hk, D, table.shape[1]))
@@ -227,8 +228,9 @@ def test_a_nan_value_reaches_only_the_rows_that_see_it(D, window, sinks, wide):
 def test_starts_that_fall_or_leave_the_rows(wide):
     """Rows never belong to two sequences, and none outside q is touched."""
     rng = np.random.default_rng(7)
-    D, Hq, Hk, N, lens = 64, 4, 2, 50, [70, 80, 90, 100]
-    table, cache, qkv, _ = _inputs(rng, "f16", D, Hq, Hk, [N], lens, wide, pad=0)
+    D, Hq, Hk, lens = 64, 4, 2, [70, 80, 90, 100]
+    table, cache, qkv, _ = _inputs(rng, "f16", D, Hq, Hk, [50], lens, wide, pad=0)
+    N = len(qkv)
     q = qkv.cuda()[:, :Hq * D].unflatten(-1, (Hq, D))
     args = (_cuda(cache), _cuda(table), _cuda(np.array(lens, np.int32)))
     ws = sk.new_workspace(sk.kv4_attention_chunk_workspace_bytes(N, 4, Hq, Hk, D, table.shape[1]))
@@ -237,15 +239,15 @@ def test_starts_that_fall_or_leave_the_rows(wide):
         out, lse = torch.full(q.shape, 3.0, dtype=torch.float16, device="cuda"), torch.full(q.shape[:2], 3.0, device="cuda")
         sk.kv4_attention_chunk(q, _cuda(np.array(starts, np.int32)), *args, out, lse=lse, workspace=ws)
         return out, lse
-    for bad, good in (([10, 30, 20, 25, 40], [10, 30, 30, 30, 40]), ([-5, 5, 2 ** 31 - 1, 7, 60], [0, 5, 50, 50, 50]),
-                      ([-2 ** 31] * 5, [0] * 5), ([60, 10, 20, 30, 40], [50] * 5), ([5, 4, 3, 2, 50], [5, 5, 5, 5, 50])):
+    for bad, good in (([10, 30, 20, 25, 40], [10, 30, 30, 30, 40]), ([-5, 5, 2 ** 31 - 1, 7, N + 10], [0, 5, N, N, N]),
+                      ([-2 ** 31] * 5, [0] * 5), ([N + 10, 10, 20, 30, 40], [N] * 5), ([5, 4, 3, 2, 50], [5, 5, 5, 5, 50])):
         for a, b in zip(run(bad), run(good)):
             assert torch.equal(a, b), bad
     assert (run([0] * 5)[0] == 3).all()
 
 
 @gpu
-@WIDE
+@pytest.mark.parametrize("wide", [False, True])
 def test_lens_beyond_the_table_and_below_zero_are_clamped(wide):
     rng = np.random.default_rng(9)
     D, Hk, Hq = 64, 1, 4
@@ -311,6 +313,7 @@ def test_offsets_past_32_bits(wide):
     pages = (1 << 32) // (Hk * 72 * D) + 64
     rng = np.random.default_rng(8)
     table, small, qkv, starts = _inputs(rng, "f16", D, Hq, Hk, [T], [n], wide, pad=0)
+    N = len(qkv)
     small, none = small[:4], np.full((1, table.shape[1] - 4 if wide else 0), -1, np.int32)
     table = np.concatenate([np.arange(4, dtype=np.int32)[None], none], 1)
     cache = torch.empty((pages, Hk, 72 * D), dtype=torch.uint8, device="cuda")
@@ -319,12 +322,12 @@ def test_offsets_past_32_bits(wide):
         cache[p] = _cuda(small[i])
     ids = np.concatenate([ids, none], 1)
     # Rows far apart: the last of a view whose elements span more than 2^32 bytes.
-    far = torch.empty((T, (1 << 32) // (2 * (T - 1)) // 8 * 8 + 4096), dtype=torch.float16, device="cuda")
+    far = torch.empty((N, (1 << 32) // (2 * (N - 1)) // 8 * 8 + 4096), dtype=torch.float16, device="cuda")
     far[:, :Hq * D] = qkv.cuda()[:, :Hq * D]
     got = []
     for q, c, t in ((far, cache, ids), (qkv.cuda(), _cuda(small), table)):
-        out, lse = torch.empty((T, Hq, D), dtype=torch.float16, device="cuda"), torch.empty((T, Hq), device="cuda")
-        ws = sk.new_workspace(sk.kv4_attention_chunk_workspace_bytes(T, 1, Hq, Hk, D, t.shape[1]))
+        out, lse = torch.zeros((N, Hq, D), dtype=torch.float16, device="cuda"), torch.zeros((N, Hq), device="cuda")
+        ws = sk.new_workspace(sk.kv4_attention_chunk_workspace_bytes(N, 1, Hq, Hk, D, t.shape[1]))
         sk.kv4_attention_chunk(q[:, :Hq * D].unflatten(-1, (Hq, D)), _cuda(starts), c, _cuda(t), _cuda(np.array([n], np.int32)), out, lse=lse, workspace=ws)
         got.append((out, lse))
     for a, b in zip(*got):
@@ -430,8 +433,9 @@ def test_many_slots_of_little_weight_count(D, call):
 
 
 @gpu
+@pytest.mark.parametrize("tall", [False, True])
 @pytest.mark.parametrize("B, longest", [(300, 190000), (1100, 500), (1500, 100000)])
-def test_many_sequences(B, longest):
+def test_many_sequences(B, longest, tall):
     """More tiles than the plan has threads, more sequences than it holds at once, and one that is much longer than all
     others, or not; some have no new token, and pages are shared."""
     rng = np.random.default_rng(B)
@@ -445,12 +449,15 @@ def test_many_sequences(B, longest):
     table = rng.integers(-1, len(cache), (B, width)).astype(np.int32)
     starts = np.concatenate([[2], 2 + np.cumsum(chunks)]).astype(np.int32)
     N = int(starts[-1]) + 3
-    q = torch.from_numpy(rng.standard_normal((N, Hq, D)) * 2.0).half()
+    used = torch.from_numpy(rng.standard_normal((N, Hq, D)) * 2.0).half()
+    N += 500 * B if tall else 0
+    q = torch.zeros((N, Hq, D), dtype=torch.float16, device="cuda")
+    q[:len(used)] = used
     out, lse = torch.full((N, Hq, D), 3.0, dtype=torch.float16, device="cuda"), torch.full((N, Hq), 3.0, device="cuda")
     ws = sk.new_workspace(sk.kv4_attention_chunk_workspace_bytes(N, B, Hq, Hk, D, width))
-    sk.kv4_attention_chunk(q.cuda(), _cuda(starts), _cuda(cache), _cuda(table), _cuda(lens.astype(np.int32)), out, lse=lse, scale=0.125, workspace=ws)
+    sk.kv4_attention_chunk(q, _cuda(starts), _cuda(cache), _cuda(table), _cuda(lens.astype(np.int32)), out, lse=lse, scale=0.125, workspace=ws)
     for t in (out, lse):
-        assert (t[:2] == 3).all() and (t[N - 3:] == 3).all()
+        assert (t[:2] == 3).all() and (t[starts[-1]:] == 3).all()
     some = [(b, i, rng.integers(Hq)) for b in [at, *rng.permutation(B)[:150], 0, B - 1] for i in range(chunks[b])]
-    _check("f16", out, lse, _refs(some, cache, table, lens, starts, q.double().numpy(), Hq, Hk, D, 0.125, 1.0, 1.0, 0, 0))
-    assert not (out[2:N - 3] == 3).all(-1).any()
+    _check("f16", out[:len(used)], lse[:len(used)], _refs(some, cache, table, lens, starts, used.double().numpy(), Hq, Hk, D, 0.125, 1.0, 1.0, 0, 0))
+    assert not (out[2:starts[-1]] == 3).all(-1).any()
