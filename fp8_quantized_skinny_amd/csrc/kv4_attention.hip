@@ -438,10 +438,15 @@ __device__ __forceinline__ Share chunk_share(const AttendArgs& a, int rows, int 
       const auto its = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
       s.any = true;
       s.b = b0 + l;
-      s.splits = its(all) / its(q.n);
       const int in = at - (its(upto) - its(all));  // among the sequence's shares
-      s.qg = in / s.splits;
-      const int each = (its(q.pages) + s.splits - 1) / s.splits, share = in % s.splits;
+      s.qg = in;
+      int each = 0, share = 0;
+      if (chunk) {
+        s.splits = its(all) / its(q.n);
+        s.qg = in / s.splits;
+        share = in - s.qg * s.splits;
+        each = (its(q.pages) + s.splits - 1) / s.splits;
+      }
       of->group = its(group) - its(q.n) + s.qg;
       s.p0 = share * each;
       of->end = share == s.splits - 1 ? 0x7FFFFFFF : s.p0 + each;  // the last one's: what there is
