@@ -1047,7 +1047,7 @@ hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type,
 // to 128 pages.  The two meet near 96 pages there and for D = 64 (29 us), and
 // between 96 and 128 for D = 256.
 //
-// Over more pages these are split into shares.  Of many pages a group of 48 rows
+// Over more pages, or with more groups, these are split into shares.  Of many pages a group of 48 rows
 // (32 at D = 256) takes kGroup[D] ns a page and head of the whole card's time, a tile
 // of 256 rows with few of them in use kTileOf[D], which has a plan and other
 // beginnings to make up for, kFixed ns; shares are coarse where there are many groups.
@@ -1059,9 +1059,14 @@ hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type,
 //   16 x 48                   39.3  68.0   87.6   194    296   691     246   402
 //   16 x 120 or 126           89.0  74.4    260   209    919   718     461   438
 //   16 x 252                   126  91.4    391   254   1486   964     886   545
+// Every workgroup looks through the lengths of all sequences, which costs more than
+// it brings when these are many (8 heads of 4, rows of 8 tokens, up to 97 pages: 512
+// sequences 1150 us against 1435 in tiles, 1024 3208 against 2746; up to 32 pages:
+// 128 sequences 150 against 166, 256 367 against 302).
 SmallChunk kv4_small_chunk(int N, int B, int G, int Hk, int D, int64_t pages) {
-  constexpr int kCUs = 256, kMostPages = 96;
+  constexpr int kCUs = 256, kMostPages = 96, kFewSequences = 128, kMostSequences = 512;
   SmallChunk s{};
+  if (B > kMostSequences) return s;
   const int64_t busy = N < B ? N : B, rows = static_cast<int64_t>(N) * G;  // sequences with rows
   const auto groups = [&](int height) { return (rows + busy * (height - 1)) / height; };
   if (pages <= kMostPages)
@@ -1074,7 +1079,7 @@ SmallChunk kv4_small_chunk(int N, int B, int G, int Hk, int D, int64_t pages) {
   const int64_t mean = (rows + busy - 1) / busy;  // rows of a sequence
   const int mt = mean < max_tiles(D) * 16 ? static_cast<int>((mean + 15) / 16) : max_tiles(D);
   const int64_t tall = groups(mt * 16);
-  if (pages <= kMostPages || tall * (pages + 1) > INT32_MAX) return s;
+  if ((pages <= kMostPages && B > kFewSequences) || tall * (pages + 4) > INT32_MAX) return s;
   constexpr double kGroup[] = {1.6, 2.25, 3.2}, kTileOf[] = {3.9, 5.5, 11.3}, kFixed[] = {16000.0, 16000.0, 35000.0};
   const int size = D / 128;  // 0, 1, 2
   const int64_t whole = busy * ((mean + mt * 16 - 1) / (mt * 16));

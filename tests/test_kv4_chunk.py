@@ -434,7 +434,7 @@ def test_many_slots_of_little_weight_count(D, call):
 
 @gpu
 @pytest.mark.parametrize("tall", [False, True])
-@pytest.mark.parametrize("B, longest", [(300, 190000), (1100, 500), (1500, 100000)])
+@pytest.mark.parametrize("B, longest", [(300, 190000), (500, 700), (1100, 500), (1500, 100000)])
 def test_many_sequences(B, longest, tall):
     """More tiles than the plan has threads, more sequences than it holds at once, and one that is much longer than all
     others, or not; some have no new token, and pages are shared."""
