@@ -157,19 +157,38 @@ bool same_heads(const Heads& a, const Heads& b, int B, int T) {
          (T == 1 || a.r->row == b.r->row) && (a.H == 1 || a.r->head == b.r->head);
 }
 // Whether two views share no element, as far as that shows: they lie one behind
-// the other, or side by side in sequences or in tokens of the same strides.
+// the other; or side by side in the step of a dimension that both take alike, so
+// that each has its own part of every step; or both take both steps alike and no
+// token of one comes to lie on one of the other.  (Side by side within the lesser
+// step does not do for that: where the greater is no multiple of it, a token may
+// lie on one of another sequence.)
 bool disjoint(const Heads& a, const Heads& b, int B, int T, int D) {
   const int64_t x = reinterpret_cast<intptr_t>(a.r->data), y = reinterpret_cast<intptr_t>(b.r->data);
-  if (x + 2 * view_extent(a, B, T, D) <= y || y + 2 * view_extent(b, B, T, D) <= x) return true;
   if (x > y) return disjoint(b, a, B, T, D);
-  if (B > 1 && a.r->sequence != b.r->sequence) return false;
-  const int64_t at = (y - x) / 2;
-  if (at >= view_extent(a, 1, T, D) && at + view_extent(b, 1, T, D) <= a.r->sequence) return true;
-  if (T > 1 && a.r->row != b.r->row) return false;
-  int64_t step = INT64_MAX;
-  if (B > 1) step = std::min(step, a.r->sequence);
-  if (T > 1) step = std::min(step, a.r->row);
-  return at >= token_extent(a, D) && at + token_extent(b, D) <= step;
+  if (x + 2 * view_extent(a, B, T, D) <= y) return true;
+  const int64_t at = (y - x) / 2, a_token = token_extent(a, D), b_token = token_extent(b, D);
+  const auto beside = [&](int64_t a_extent, int64_t b_extent, int64_t step) { return at >= a_extent && at + b_extent <= step; };
+  const bool sequences = B == 1 || a.r->sequence == b.r->sequence, rows = T == 1 || a.r->row == b.r->row;
+  if (B > 1 && sequences && beside(view_extent(a, 1, T, D), view_extent(b, 1, T, D), a.r->sequence)) return true;
+  if (T > 1 && rows && beside(view_extent(a, B, 1, D), view_extent(b, B, 1, D), a.r->row)) return true;
+  if (!sequences || !rows) return false;
+  const auto nested = [&](int64_t less, int count, int64_t more) {
+    return beside(a_token, b_token, less) && more >= less * (count - 1) + at + b_token;
+  };
+  if (B > 1 && T > 1 && (nested(a.r->row, T, a.r->sequence) || nested(a.r->sequence, B, a.r->row))) return true;
+  // From a token of a to one of b: at, i steps in the dimension with fewer, and n in the other.
+  const bool fewer = B <= T;
+  const int few = fewer ? B : T, many = fewer ? T : B;
+  const int64_t few_step = fewer ? a.r->sequence : a.r->row, step = fewer ? a.r->row : a.r->sequence;
+  if (many == 1) return at >= a_token;
+  if (step == 0) return false;
+  for (int64_t i = 1 - few; i < few; ++i) {
+    const int64_t from = at + i * few_step, before = -b_token - from;
+    const int64_t n = before / step - (before % step < 0) + 1;  // the least that ends behind the token of a's beginning
+    const int64_t least = n < 1 - many ? 1 - many : n;
+    if (least < many && from + least * step < a_token) return false;
+  }
+  return true;
 }
 
 // Whether an output of a chunk call lies on an input or on the other output; out
