@@ -136,15 +136,14 @@ int64_t token_extent(const Heads& v, int D) { return (v.H - 1) * (v.H > 1 ? v.r-
 int64_t view_extent(const Heads& v, int B, int T, int D) {
   return (B > 1 ? (B - 1) * v.r->sequence : 0) + (T > 1 ? (T - 1) * v.r->row : 0) + token_extent(v, D);
 }
-// Whether every head has a place of its own: ordered by stride, each dimension
-// steps over all of those before it.
-bool apart(const Heads& v, int B, int T, int D) {
+// Whether every head of `extent` elements has a place of its own: ordered by
+// stride, each dimension steps over all of those before it.
+bool apart(const Heads& v, int B, int T, int64_t extent) {
   struct Dim {
     int64_t stride;
     int count;
   } d[3] = {{v.r->sequence, B}, {v.r->row, T}, {v.r->head, v.H}};
   std::sort(d, d + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
-  int64_t extent = D;
   for (const Dim& x : d) {
     if (x.count == 1) continue;
     if (x.stride < extent) return false;
@@ -158,8 +157,9 @@ bool same_heads(const Heads& a, const Heads& b, int B, int T) {
 }
 // Whether two views share no element, as far as that shows: they lie one behind
 // the other; or side by side in the step of a dimension that both take alike, so
-// that each has its own part of every step; or both take both steps alike and no
-// token of one comes to lie on one of the other.  (Side by side within the lesser
+// that each has its own part of every step; or both take the sequences' and the
+// tokens' steps alike, and either the heads' too, which lie in turn, or no token
+// of one comes to lie on one of the other.  (Side by side within the lesser
 // step does not do for that: where the greater is no multiple of it, a token may
 // lie on one of another sequence.)
 bool disjoint(const Heads& a, const Heads& b, int B, int T, int D) {
@@ -172,8 +172,11 @@ bool disjoint(const Heads& a, const Heads& b, int B, int T, int D) {
   if (B > 1 && sequences && beside(view_extent(a, 1, T, D), view_extent(b, 1, T, D), a.r->sequence)) return true;
   if (T > 1 && rows && beside(view_extent(a, B, 1, D), view_extent(b, B, 1, D), a.r->row)) return true;
   if (!sequences || !rows) return false;
-  const auto nested = [&](int64_t less, int count, int64_t more) {
-    return beside(a_token, b_token, less) && more >= less * (count - 1) + at + b_token;
+  // Heads of the two in turn: those of both together have places of their own.
+  const Heads& more = a.H < b.H ? b : a;
+  if ((a.H == 1 || b.H == 1 || a.r->head == b.r->head) && at >= D && apart(more, B, T, at + D)) return true;
+  const auto nested = [&](int64_t less, int count, int64_t greater) {
+    return beside(a_token, b_token, less) && greater >= less * (count - 1) + at + b_token;
   };
   if (B > 1 && T > 1 && (nested(a.r->row, T, a.r->sequence) || nested(a.r->sequence, B, a.r->row))) return true;
   // From a token of a to one of b: at, i steps in the dimension with fewer, and n in the other.

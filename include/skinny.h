@@ -667,8 +667,8 @@ int kv4_evict(const kv4_cache* cache, const float* acc, const kv4_cache* dst,
  *   q, k, q_out, k_out : [B][T][Hq or Hk][D] of `type` by strides, as kv4_rows.
  *          q_out may be q, and k_out k: the same pointer and strides.  Otherwise
  *          no output may share memory with an input or with the other output
- *          (views side by side in the tokens or sequences of one buffer serve):
- *          SKINNY_EINVAL.
+ *          (views side by side in the sequences or tokens of one buffer, or whose
+ *          heads lie there in turn, serve): SKINNY_EINVAL.
  *   positions : device, int32 [B][T], any values.
  *   inv_freq  : device, fp32 [rot/2], radians per position (NULL if rot is 0).
  *   q_weight, k_weight : device, fp32 [D], each may be NULL.

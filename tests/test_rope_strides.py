@@ -97,6 +97,20 @@ def test_slices_of_one_buffer_serve(order, B, T):
 
 
 @gpu
+@pytest.mark.parametrize("order, B, T", [*APART, ("BTHD", 1, 1), ("BTHD", 1, 7), ("BTHD", 7, 1)])
+def test_heads_in_turn_serve(order, B, T):
+    """A head's query, key and value behind one another, and the next head's behind these."""
+    sizes = dict(B=B, T=T, H=3, D=3 * D)
+    buffer = torch.randn([sizes[c] for c in order], generator=torch.Generator().manual_seed(0)).half().cuda()
+    q, k, v = buffer.permute(*(order.index(c) for c in "BTHD")).split(D, 3)
+    values = v.clone()
+    _check(q, k, torch.empty_like(q), torch.empty_like(k))
+    _check(q, k, q, k)
+    _check(q, k[:, :, :2], q, k[:, :, :2])
+    assert torch.equal(v, values)
+
+
+@gpu
 @pytest.mark.parametrize("B, T, at, sequence, row", [(2, 2, 192, 384, 960), (3, 2, 128, 256, 832), (2, 3, 64, 1000, 256), (4, 5, 128, 1408, 256)])
 def test_steps_that_cross_without_meeting_serve(B, T, at, sequence, row):
     for a, b in itertools.combinations((0, at), 2):
