@@ -550,14 +550,14 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
   }
   __syncthreads();
 
-  float cm[MT], m[MT], l[MT], l_over[MT];  // l_over: what rounding put into l beyond the weights' sum (windows)
+  float cm[MT], m[MT], l[MT], l_new[MT];  // l_new: what is not in l yet, of the last pages and of what rounding took
   f32x4 o[MT][DB];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     cm[mt] = fmaxf(a.scale * a.c.gk * kLog2e * factor[mt * 16 + c], kMinNormal);
     m[mt] = -INFINITY;
     l[mt] = 0.0f;
-    l_over[mt] = 0.0f;
+    l_new[mt] = 0.0f;
 #pragma unroll
     for (int s = 0; s < DB; ++s) o[mt][s] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
@@ -626,7 +626,7 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
         const float alpha = up ? __builtin_amdgcn_exp2f(m[mt] - to) : 1.0f;
         m[mt] = to;
         l[mt] *= alpha;
-        if constexpr (WINDOW) l_over[mt] *= alpha;
+        l_new[mt] *= alpha;
 #pragma unroll
         for (int d = 0; d < DB; ++d) o[mt][d] *= alpha;
       }
@@ -635,24 +635,27 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       const float lifted = m[mt] == -INFINITY ? 0.0f : m[mt] - kLift;
-      float sum = WINDOW ? 0.0f : l[mt];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][mt][e], cm[mt], -lifted));
-          sum += w;
+          l_new[mt] += w;
           p[j / 2][mt][(j % 2) * 4 + e] = static_cast<_Float16>(w);
         }
-      if constexpr (WINDOW) {  // what an addition loses goes into the next one, as in kv4_chunk.hip
-        sum -= l_over[mt];
-        const float more = l[mt] + sum;
-        l_over[mt] = (more - l[mt]) - sum;
-        l[mt] = more;
-      } else {
-        l[mt] = sum;
-      }
       __builtin_amdgcn_sched_barrier(0);
+    }
+    // A long share's slots may each be too small for the sum of the pages before (512 sequences of 4000 pages, most weight in
+    // the first slot: the log-sum was off by 1.6e-4 with one sum).  So l grows by a page at a time, and what its rounding takes
+    // goes into the next; with three tiles of rows, which the VALU bounds, by four pages (120000 slots of four rows of 12
+    // heads: 153 us, page by page 156; with two tiles at D = 256, eight rows of six, 2000 slots, 39.5 and 39.1 with the weights).
+    if (WINDOW || MT < 3 || (page / kWaves) % 4 == 3) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const float more = l[mt] + l_new[mt];
+        l_new[mt] -= more - l[mt];
+        l[mt] = more;
+      }
     }
     if constexpr (kLateKeys) k.load(next.block, lane);
 #pragma unroll
@@ -691,7 +694,7 @@ __global__ __launch_bounds__(kThreads, attend_per_cu(D, MT)) void attend(const A
   // The wavefronts' sums meet in LDS, one group of 16 queries at a time.
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    const float total = sum_over_rows(l[mt]);
+    const float total = sum_over_rows(l[mt] + l_new[mt]);
     if (g == 0) {
       stat[wave][mt * 16 + c][0] = m[mt];
       stat[wave][mt * 16 + c][1] = total;
