@@ -239,7 +239,8 @@ __device__ __forceinline__ f16x2 e2m1_pos(u32x2 pair, int s) {  // position s (0
 // Slots past the sequence's length hold anything: their V scales become 0, so
 // that the codes stand for 0 and not for NaN.  A NaN in a slot that only later
 // rows see must not reach the others through a weight of 0: such scales become
-// 0 too, and the rows that do see the slot are made NaN by hand.
+// 0 too, and the sums of the rows that do see the slot are made NaN by hand, where
+// the scale is theirs.
 template <bool WINDOW, int D, int MT>
 __device__ __forceinline__ void clean_values(const AttendArgs& a, VRegs<D>& v, int first, int len, int lane,
                                              const int (&limit)[MT], f32x4 (&o)[MT][D / 16]) {
@@ -258,41 +259,24 @@ __device__ __forceinline__ void clean_values(const AttendArgs& a, VRegs<D>& v, i
       }
   }
   if (!__any(bad != 0u)) return;
-  if constexpr (WINDOW) {
-    // Row r of the sums is of the values that lanes r, 16 + r, .. hold: these rows, and no others of the query, are
-    // made NaN where it sees the token.
-    for (int rg = 0; rg < 4; ++rg)
-      for (int tg = 0; tg < 4; ++tg)
+  // Row r of the sums is of the values that lanes r, 16 + r, .. hold: these rows, and no others of the query, are
+  // made NaN where it sees the token.
+  for (int rg = 0; rg < 4; ++rg)
+    for (int tg = 0; tg < 4; ++tg)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t of = __builtin_amdgcn_readlane(bad, 16 * tg + 4 * rg + e);
-          if (!of) continue;
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t of = __builtin_amdgcn_readlane(bad, 16 * tg + 4 * rg + e);
+        if (!of) continue;
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            bool seen = false;
-            for (int i = 0; i < 16; ++i) seen |= ((of >> i) & 1u) && !hidden<true>(a, first + 16 * (i / 4) + 4 * tg + i % 4, limit[mt]);
-            if (seen && g == rg) {
+        for (int mt = 0; mt < MT; ++mt) {
+          bool seen = false;
+          for (int i = 0; i < 16; ++i) seen |= ((of >> i) & 1u) && !hidden<WINDOW>(a, first + 16 * (i / 4) + 4 * tg + i % 4, limit[mt]);
+          if (seen && g == rg) {
 #pragma unroll
-              for (int s = 0; s < D / 16; ++s) o[mt][s][e] = NAN;
-            }
+            for (int s = 0; s < D / 16; ++s) o[mt][s][e] = NAN;
           }
         }
-    return;
-  }
-#pragma unroll
-  for (int s = 1; s < 16; s <<= 1) bad |= __shfl_xor(bad, s);  // over the lanes of the same four tokens
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    bool seen = false;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      seen |= ((bad >> i) & 1u) && !hidden<WINDOW>(a, first + 16 * (i / 4) + 4 * g + i % 4, limit[mt]);
-    // Lanes of one query hold different positions: all four rows of lanes.
-    if (max_over_rows(seen ? 1.0f : 0.0f) > 0.0f) {
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s) o[mt][s] = f32x4{NAN, NAN, NAN, NAN};
-    }
-  }
+      }
 }
 
 // A workgroup's share of the work: pages p0 .. p1 of one segment (sequence b,

@@ -557,11 +557,11 @@ int kv4_read(const kv4_cache* cache, void* k, void* v, int type, int n,
  * fp16, relative to the row's greatest.  bf16 queries are scaled to fp16's
  * range by a power of two per row: values down to 2^-31 of the row's greatest
  * (or of 2^-100, if that is more) are exact, and smaller ones are off by 2^-39 of
- * it at most.  A NaN among the values of a slot that only some rows see
- * makes those rows NaN and no others.  A NaN among the scores of a row (of its
- * query, or of the key of a slot that it sees) makes its out and lse NaN.  A row
- * whose scores are all -inf, which takes an infinite query, has no weight
- * anywhere: its out is zero and its lse -inf. */
+ * it at most.  A NaN among the values of a slot (a group of 16 positions, as held)
+ * makes those positions NaN in the rows that see the slot, and nothing else.  A
+ * NaN among the scores of a row (of its query, or of the key of a slot that it
+ * sees) makes its out and lse NaN.  A row whose scores are all -inf, which takes
+ * an infinite query, has no weight anywhere: its out is zero and its lse -inf. */
 int kv4_attention(const kv4_cache* cache, const kv4_rows* q, int type, int T,
                   int Hq, float scale, void* out, float* lse, void* workspace,
                   size_t workspace_bytes, hipStream_t stream);
