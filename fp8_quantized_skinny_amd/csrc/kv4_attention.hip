@@ -472,7 +472,7 @@ constexpr int attend_per_cu(int D, int MT) { return D == 256 && MT == 2 ? 1 : (D
 // What bounds it: with one tile of queries, memory (16 sequences of 30000 ..
 // 32768 tokens, four heads of 128: 290 MB in 52 us, 5.5 TB/s, where a large copy
 // moves 4.7); with three, memory and the widening and softmax about equally
-// (eight sequences of 120000 .. 131072 tokens: 578 MB and 99 GFLOP in 145 us; the
+// (eight sequences of 120000 .. 131072 tokens: 578 MB and 99 GFLOP in 142 us; the
 // VALU is busy for 59% of the cycles and the matrix unit for 29%); short
 // sequences, latency: of one sequence of 8197 tokens' 16 us a page takes 2.6
 // and the joining of four wavefronts' sums 3.
@@ -1050,6 +1050,10 @@ hipError_t launch_kv4_attention(const kv4_cache& c, const kv4_rows& q, int type,
 // it brings when these are many (8 heads of 4, rows of 8 tokens, up to 97 pages: 512
 // sequences 1150 us against 1435 in tiles, 1024 3208 against 2746; up to 32 pages:
 // 128 sequences 150 against 166, 256 367 against 302).
+//
+// A call goes one way, by its mean: 63 single tokens over 4096 slots beside a prompt
+// of 2048 (32/8 heads of 128) have a tile each, 317 us, where the prompt alone takes
+// 130 and the tokens 49.
 SmallChunk kv4_small_chunk(int N, int B, int G, int Hk, int D, int64_t pages) {
   constexpr int kCUs = 256, kMostPages = 96, kFewSequences = 128, kMostSequences = 512;
   SmallChunk s{};

@@ -25,7 +25,7 @@
 // operations a lane and 36 KB of LDS writes.
 //
 // Bound by the matrix unit, the VALU and the power that both may draw: 8192 tokens,
-// 48 + 4 heads of 128, 810 .. 855 us, 0.98 .. 1.02 PFLOP/s of seen products at
+// 48 + 4 heads of 128, 811 .. 861 us, 0.96 .. 1.02 PFLOP/s of seen products at
 // about 1.8 GHz, where a large fp16 product reaches 1.0 PFLOP/s at first and 1.36
 // when nothing else runs for long.  The matrix unit is busy for 53% of the cycles,
 // the VALU for 58%, LDS for 37%.  Parts left out of the kernel of 852 us (for
@@ -47,8 +47,9 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kTile = 32 * kWaves;
 constexpr int kSlots = 256;  // workgroups that the CUs hold at once
 constexpr int kLeast = 16;   // fewest pages of a workgroup where tiles are cut
-constexpr int kCutPages = 6;  // what the cut tiles' parts cost a workgroup, in pages: stored by it, and read by the join
-constexpr int kBegin = 10;     // what a tile's beginning and end cost, in pages (less than kLeast; see the plan)
+// Both in pages, whatever the head size (see the plan).
+constexpr int kCutPages = 6;  // what the cut tiles' parts cost a workgroup: stored by it, and read by the join
+constexpr int kBegin = 10;    // what a tile's beginning and end cost (less than kLeast)
 constexpr int kPlanThreads = 256;
 constexpr int kPlanHeld = 1024;  // sequences whose rows and tiles the plan keeps in LDS
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -145,12 +146,18 @@ struct Sight {
 // CU waits for a last long tile (512 tokens over 120000, 24 tiles of 1883 pages a
 // head: 1754 us with each tile in six equal shares, 1442 so).  A tile counts kBegin
 // pages more than it has, or the workgroup with the shortest tiles, up to eleven of
-// them, ends last: 16 chunks of 1 .. 640 tokens over up to 9000, five draws, took
-// 514, 369, 424, 419 and 344 us with 0, 476, 343, 362, 362 and 283 with 5, 468, 338,
-// 359, 336 and 260 with 10, and 470, 341, 355, 334 and 262 with 14.  Whole tiles are
-// taken where they end kCutPages or less after the even shares: three chunks of 1500
-// .. 4100 tokens within 1024 (D = 256), 382, 360, 340 and 356 us as whole tiles (24
-// or 12 pages), 373, 331, 323 and 327 cut; 14 chunks of 1286 the same either way.
+// them, ends last.  Whole tiles are taken where they end kCutPages or less after the
+// even shares.  Three draws each of 16 chunks of 1 .. 640 tokens over up to 9000, and
+// of three of 1500 .. 4100 within 1024 (bf16, us); 14 chunks of 1286 take the same with
+// all of these:
+//   kBegin                0            5           10           14
+//   28/4 heads of 64  238 247 272  223 210 222  219 207 208  222 209 213
+//   32/8 of 128       365 385 424  337 358 359  329 346 349  336 358 347
+//   24/4 of 256       552 573 650  507 531 531  514 536 531  521 556 527
+//   kCutPages             0            6           12           24
+//   28/4 heads of 64  153 155 158  153 155 158  147 151 151  147 151 152
+//   32/8 of 128       243 259 260  243 260 260  242 260 260  244 260 260
+//   24/4 of 256       329 339 336  330 337 336  348 371 371  349 372 371
 //
 // The rows of a sequence go from its start to the next one's; a start that is not
 // in 0 .. N counts as the nearer of these, and one below an earlier start as that:

@@ -492,8 +492,9 @@ int skinny_read_probe_pattern(const void* buf, size_t bytes, int pattern,
  *            1 <= Hk <= 1024;  64 * width < 2^31.
  *   gk, gv : finite and > 0.
  * A call whose sequences, heads and pages make more workgroups than a grid
- * holds (2^24, and B * Hk < 2^22 for kv4_evict) is refused: SKINNY_ESHAPE.  So
- * is kv4_attention with B * (width + 1) >= 2^31.
+ * holds (2^24, 2^23 for kv4_attention_chunk, and B * Hk < 2^22 for kv4_evict) is
+ * refused: SKINNY_ESHAPE.  So is kv4_attention, with a window or without, with
+ * B * (width + 1) >= 2^31.
  *
  * A table entry outside 0 .. pages - 1 that a sequence's slots reach names no
  * page: nothing is read or written there, its slots are held by nobody
@@ -661,9 +662,11 @@ int kv4_evict(const kv4_cache* cache, const float* acc, const kv4_cache* dst,
  *                    y[i + rot/2] = u[i + rot/2] c_i + u[i] s_i;
  *   interleaved = 1: the same of the pairs u[2i] and u[2i + 1];
  *   y[d] = u[d] for d >= rot.
- * All of it in fp32 and the angles in fp64 (right to 2^-24 of a turn at every
- * position, for frequencies up to 1), and y rounded once.  A scaling of the positions for long contexts is
- * in inv_freq, and one of the result (YaRN's) in amplitude.
+ * All of it in fp32, the squares too (so bf16 heads are normed while these stay
+ * within fp32's range), the angles in fp64 (right to 2^-24 of a turn at every
+ * position, for frequencies up to 1), and y rounded once.  A scaling of the
+ * positions for long contexts is in inv_freq, and one of the result (YaRN's) in
+ * amplitude.
  *   q, k, q_out, k_out : [B][T][Hq or Hk][D] of `type` by strides, as kv4_rows.
  *          q_out may be q, and k_out k: the same pointer and strides.  Otherwise
  *          no output may share memory with an input or with the other output
