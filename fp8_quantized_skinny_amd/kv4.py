@@ -119,6 +119,7 @@ def rope_inv_freq(rot, base=10000.0, factor=1.0, original=0, fast=32.0, slow=1.0
         at = lambda n: rot * np.log(original / (n * 2.0 * np.pi)) / (2.0 * np.log(base))  # noqa: E731
         low, high = max(np.floor(at(fast)), 0.0), min(np.ceil(at(slow)), rot - 1.0)
         stay = 1.0 - np.clip((i - low) / max(high - low, 1e-3), 0.0, 1.0)
+        stay[i >= np.ceil(at(slow))] = 0.0  # also where the first pair itself makes too few turns
     return (freq * stay + freq / factor * (1.0 - stay)).astype(np.float32)
 
 
