@@ -109,8 +109,8 @@ def rope_inv_freq(rot, base=10000.0, factor=1.0, original=0, fast=32.0, slow=1.0
     that a model was trained on divided by factor.  With `original`, the positions it was trained on, only the pairs that turn
     fewer than `slow` times over these are divided by all of it, those of more than `fast` turns stay, and between
     them the share falls in a straight line over the pairs' indices (YaRN: Peng et al., 2023, whose amplitude is 0.1 ln(factor) + 1)."""
-    if rot < 0 or rot % 2 or base <= 1.0 or factor <= 0.0 or original < 0 or not fast > slow > 0.0:
-        raise ValueError("rot must be even, base > 1, factor > 0, original >= 0 and fast > slow > 0")
+    if rot < 0 or rot % 2 or not (1.0 < base < np.inf and 0.0 < factor < np.inf and 0.0 <= original < np.inf and 0.0 < slow < fast < np.inf):
+        raise ValueError("rot must be even, base > 1, factor > 0, original >= 0 and fast > slow > 0, all of them finite")
     i = np.arange(rot // 2, dtype=np.float64)
     freq = base ** (-2.0 * i / max(rot, 1))
     stay = np.zeros_like(freq)

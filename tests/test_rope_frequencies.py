@@ -16,3 +16,10 @@ def test_pairs_of_few_and_of_many_turns(rot, original):
     share = plain / scaled
     assert (np.abs(share[turns < 1.0] - 8.0) <= 8.0 * 2.0 ** -22).all() and (np.abs(share[turns > 32.0] - 1.0) <= 2.0 ** -22).all()
     assert (share >= 1.0 - 2.0 ** -22).all() and (share <= 8.0 + 2.0 ** -19).all()
+
+
+@pytest.mark.parametrize("name", ["base", "factor", "original", "fast", "slow"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_what_is_no_number_is_refused(name, value):
+    with pytest.raises(ValueError):
+        sk.rope_inv_freq(64, **{"factor": 2.0, "original": 4096, name: value})
